@@ -365,6 +365,120 @@ int wedlm_attention_static(int32_t batch, int32_t window, int32_t n_q_heads,
  * copy or the wait fails. */
 int wedlm_attention_static_status(void *stream, int32_t *device_error);
 
+/* ---- appending to the paged cache, attention over a shared prefix ------- */
+
+/* Rows of a caller's projection: element (b, p, head, d) is at
+ * ptr[b*batch_stride + p*row_stride + head*head_stride + d] (strides in
+ * elements, >= 0).  ptr 16-byte aligned, strides multiples of 16 bytes.  A
+ * slice of a packed q|k|v projection is one of these. */
+typedef struct wedlm_rows {
+  const void *ptr;
+  int64_t batch_stride, row_stride, head_stride;
+} wedlm_rows;
+
+/* Inputs and outputs of wedlm_append_kv (device pointers). */
+typedef struct wedlm_append_args {
+  int32_t batch;               /* B >= 1                                   */
+  int32_t rows;                /* n >= 1 rows per sequence; <= 64 with
+                                  kv_win; B*n < 2^31                       */
+  int32_t n_q_heads;           /* ignored without q                        */
+  int32_t n_kv_heads, head_dim;/* head_dim 64 or 128                       */
+  int32_t dtype;               /* WEDLM_BF16 | WEDLM_FP32                  */
+  int32_t max_pages_per_seq;   /* columns of page_table                    */
+  int32_t num_pages;           /* pages in kv_pool                         */
+  float rms_eps, rope_theta;   /* rope_theta >= 1                          */
+  wedlm_rows k, v;             /* [B][n][n_kv_heads][head_dim]             */
+  wedlm_rows q;                /* [B][n][n_q_heads][head_dim]; ptr NULL: none */
+  const void *q_norm, *k_norm; /* [head_dim] RMSNorm gains, or NULL: none  */
+  const int32_t *pos;          /* [B][n] logical positions, or NULL:
+                                  seq_len[b] + p                           */
+  const int32_t *counts;       /* [B] rows appended, 0..n, or NULL: n      */
+  const int32_t *seq_len;      /* [B] committed lengths (read only)        */
+  const int32_t *page_table;   /* [B][max_pages_per_seq]                   */
+  void *kv_pool;               /* one layer's pool                         */
+  void *q_out;                 /* [B*n][n_q_heads][head_dim]; with q only  */
+  void *kv_win;                /* [B][2][n_kv_heads][Wp][head_dim] in the page
+                                  tile layout (Wp = n rounded up to 16), or NULL */
+  int32_t *new_seq_len;        /* [B] seq_len + appended rows, or NULL; not
+                                  the same memory as seq_len               */
+  int32_t *error;              /* device word that WEDLM_DEV_* bits are OR-ed
+                                  into, or NULL; never cleared here        */
+} wedlm_append_args;
+
+/* Append keys and values to the paged cache, with the per-head RMSNorm
+ * (optional) and the rotate-half RoPE at logical positions (Key claims §4.1)
+ * applied on the way: what the step's QKV epilogue does to its projections,
+ * for callers that bring their own.  Row p of sequence b:
+ *  - q (when given) and k are normalised with q_norm / k_norm, rotated at
+ *    pos[b][p], rounded once to the dtype; v is copied;
+ *  - q goes to q_out for every row; K and V of every row go to kv_win when it
+ *    is given (rows n..Wp-1 of a block become zeros);
+ *  - for p < counts[b], K and V go to position seq_len[b] + p of the cache.
+ *    Nothing else in the pool is written.
+ * The attention that reads kv_win as the window takes the lengths before the
+ * append; once the window is left behind, new_seq_len.
+ * A row beyond the page table sets WEDLM_DEV_CAPACITY, one on a page id
+ * outside [0, num_pages) WEDLM_DEV_BAD_PAGE; either is not written.  A
+ * negative seq_len, or a count outside 0..n, sets WEDLM_DEV_BAD_SEQLEN; the
+ * former appends nothing (and its rows without `pos` rotate as if it were 0),
+ * the latter is clamped.  new_seq_len stops at the page table's capacity.
+ * No two appended rows may go to one place of the pool.  No context, workspace
+ * or allocation; calls on different streams are independent.  Returns
+ * WEDLM_ERR_INVALID_ARG (nothing enqueued) or WEDLM_ERR_CUDA. */
+int wedlm_append_kv(const wedlm_append_args *args, void *stream);
+
+/* Inputs and outputs of wedlm_shared_attention (device pointers). */
+typedef struct wedlm_shared_attn_args {
+  int32_t batch;               /* B, 1..1024                               */
+  int32_t window;              /* W, 1..64 query rows per sequence         */
+  int32_t n_q_heads, n_kv_heads; /* G = n_q_heads / n_kv_heads, 1..128     */
+  int32_t head_dim;            /* 64 or 128                                */
+  int32_t dtype;               /* WEDLM_BF16 | WEDLM_FP32                  */
+  int32_t n_shared_pages;      /* S >= 0 pages of shared prefix            */
+  int32_t max_pages_per_seq;   /* columns of page_table, 1..2^26           */
+  int32_t num_pages;           /* pages in kv_pool                         */
+  const void *q;               /* [B*W][n_q_heads][head_dim], RoPE applied */
+  const void *kv_pool;         /* one layer's pool                         */
+  const int32_t *shared_pages; /* [S] pages of positions 0..16S-1 (NULL when S = 0) */
+  const int32_t *page_table;   /* [B][max_pages_per_seq]                   */
+  const int32_t *seq_len;      /* [B] cached lengths, shared part included */
+  const void *kv_win;          /* [B][2][n_kv_heads][Wp][head_dim] tile layout */
+  void *o;                     /* [B*W][n_q_heads*head_dim]                */
+  void *workspace;             /* 256-byte aligned                         */
+  size_t workspace_bytes;      /* at least wedlm_shared_attention_workspace */
+  int32_t *error;              /* as in wedlm_append_args                  */
+} wedlm_shared_attn_args;
+
+/* Bytes of workspace a wedlm_shared_attention call of these sizes needs (only
+ * the sizes of `args` are read).  0 for sizes it does not take. */
+size_t wedlm_shared_attention_workspace(const wedlm_shared_attn_args *args);
+
+/* Window attention for a batch whose sequences share a long prefix: what
+ * wedlm_attention computes (paged causal GQA attention of the W window rows,
+ * Key claims §3.2, §5.2), with positions 0..16S-1 held once, in the pages
+ * shared_pages names, and attended to by all rows of the batch together, so
+ * that their K/V are read once and not once per sequence.
+ *  - A sequence with seq_len[b] >= 16*S takes part: its positions 0..16S-1
+ *    are the shared pages (columns 0..S-1 of its page-table row are not
+ *    read), the later ones its own pages.  A shorter sequence (a padded slot
+ *    of length 0, say) reads all of its positions from its own pages.
+ *  - Positions at or beyond seq_len and window rows at or beyond W may hold
+ *    anything, infinities and NaN included: they are left out.  A V value of
+ *    a window row that is not finite reaches the earlier rows of its sequence
+ *    too (probability 0 times it); no other sequence.
+ *  - Page ids outside [0, num_pages) read as zeros and set WEDLM_DEV_BAD_PAGE;
+ *    a negative length counts as 0 and sets WEDLM_DEV_BAD_SEQLEN; one beyond
+ *    the page table is cut to it and sets WEDLM_DEV_CAPACITY; a bounded wait
+ *    that expires (2 s) leaves o unspecified and sets WEDLM_DEV_TIMEOUT.
+ *  - The workspace needs no initial contents and keeps none between calls;
+ *    calls that may overlap on the GPU (two streams, two captured graphs)
+ *    need one each.  No context and no allocation.  The result is the same,
+ *    bit for bit, whenever the inputs are.
+ *  - q, kv_pool, kv_win and o are 16-byte aligned and contiguous.
+ * Returns WEDLM_ERR_INVALID_ARG (nothing enqueued), WEDLM_ERR_CAPACITY for a
+ * workspace that is too small, or WEDLM_ERR_CUDA. */
+int wedlm_shared_attention(const wedlm_shared_attn_args *args, void *stream);
+
 /* ---- failure detection self-test ---------------------------------------- */
 
 /* Self-test of the bounded waits every kernel uses (failure detection

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int32, c_void_p
+from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libwedlm.so")
@@ -28,7 +28,8 @@ EXPORTED = ["wedlm_create", "wedlm_destroy", "wedlm_last_error", "wedlm_get_stat
             "wedlm_launches_per_step", "wedlm_step", "wedlm_reorder_embed",
             "wedlm_layer", "wedlm_attention", "wedlm_lm_head", "wedlm_attention_static",
             "wedlm_attention_static_status", "wedlm_selftest_bounded_wait",
-            "wedlm_prefill", "wedlm_generate", "wedlm_dual_stream_attention"]
+            "wedlm_prefill", "wedlm_generate", "wedlm_dual_stream_attention",
+            "wedlm_append_kv", "wedlm_shared_attention", "wedlm_shared_attention_workspace"]
 
 
 class Config(ctypes.Structure):
@@ -77,6 +78,28 @@ class StepOut(ctypes.Structure):
         "filled", "rows", "logits", "hidden")]
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [("ptr", c_void_p), ("batch_stride", c_int64), ("row_stride", c_int64),
+                ("head_stride", c_int64)]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in (
+        "batch", "rows", "n_q_heads", "n_kv_heads", "head_dim", "dtype", "max_pages_per_seq",
+        "num_pages")] + [("rms_eps", c_float), ("rope_theta", c_float),
+                         ("k", Rows), ("v", Rows), ("q", Rows)] + [(n, c_void_p) for n in (
+        "q_norm", "k_norm", "pos", "counts", "seq_len", "page_table", "kv_pool", "q_out", "kv_win",
+        "new_seq_len", "error")]
+
+
+class SharedAttnArgs(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in (
+        "batch", "window", "n_q_heads", "n_kv_heads", "head_dim", "dtype", "n_shared_pages",
+        "max_pages_per_seq", "num_pages")] + [(n, c_void_p) for n in (
+        "q", "kv_pool", "shared_pages", "page_table", "seq_len", "kv_win", "o", "workspace")] + [
+        ("workspace_bytes", c_size_t), ("error", c_void_p)]
+
+
 def load_library(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
@@ -109,6 +132,10 @@ def load_library(path: str = LIB_PATH):
                                   c_int32, POINTER(c_void_p), c_void_p, c_void_p]
     lib.wedlm_generate.argtypes = [c_void_p, POINTER(GenIn), c_void_p]
     lib.wedlm_dual_stream_attention.argtypes = [c_void_p, c_int32, c_int32] + [c_void_p] * 5
+    lib.wedlm_append_kv.argtypes = [POINTER(AppendArgs), c_void_p]
+    lib.wedlm_shared_attention.argtypes = [POINTER(SharedAttnArgs), c_void_p]
+    lib.wedlm_shared_attention_workspace.argtypes = [POINTER(SharedAttnArgs)]
+    lib.wedlm_shared_attention_workspace.restype = c_size_t
     return lib
 
 
@@ -385,6 +412,178 @@ def attention_static(window, n_q_heads, n_kv_heads, max_pages_per_seq, num_pages
         _stream_handle(stream))
     if rc != OK:
         raise WedlmError(rc, "wedlm_attention_static failed")
+
+
+def _bad_arg(msg):
+    return WedlmError(ERR_INVALID_ARG, msg)
+
+
+def _dtype_code(t):
+    import torch
+    code = {torch.bfloat16: BF16, torch.float32: FP32}.get(t.dtype)
+    if code is None:
+        raise _bad_arg(f"tensors are bfloat16 or float32, not {t.dtype}")
+    return code
+
+
+def _take(name, t, like, dtype, shape=None, optional=False):
+    """Pointer of a contiguous tensor on `like`'s device, checked."""
+    if t is None:
+        if optional:
+            return None
+        raise _bad_arg(f"{name} is missing")
+    if t.device != like.device or t.dtype != dtype or not t.is_contiguous():
+        raise _bad_arg(f"{name} must be a contiguous {dtype} tensor on {like.device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise _bad_arg(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _take_rows(name, t, like, batch, rows):
+    """wedlm_rows of a [batch][rows][heads][head_dim] tensor with dense dims."""
+    if t.device != like.device or t.dtype != like.dtype or t.dim() != 4 or \
+            t.shape[0] != batch or t.shape[1] != rows or t.shape[3] != like.shape[3] or \
+            t.stride(3) != 1:
+        raise _bad_arg(f"{name} must be [{batch}][{rows}][heads][{like.shape[3]}] like k, its "
+                       "last dim dense")
+    # a dim of one element has no stride of its own
+    sb, sr, sh = (t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
+    return Rows(t.data_ptr(), sb, sr, sh)
+
+
+def _pool_pages(pool, n_kv, hd):
+    per = 2 * n_kv * 16 * hd
+    if pool.numel() == 0 or pool.numel() % per:
+        raise _bad_arg(f"the pool must hold whole pages of {per} values")
+    return pool.numel() // per
+
+
+def _launch(fn, args, device, stream):
+    """Call a context-free entry point on `device`."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return fn(ctypes.byref(args), _stream_handle(stream))
+    with torch.cuda.device(device):
+        return fn(ctypes.byref(args), _stream_handle(stream))
+
+
+def append_kv(k, v, pool, page_table, seq_len, counts=None, pos=None, q=None, q_out=None,
+              kv_win=None, k_norm=None, q_norm=None, rms_eps=1e-6, rope_theta=1e6,
+              new_seq_len=None, error=None, stream=None):
+    """wedlm_append_kv: normalise (optional) and rotate q and k rows, write K/V
+    to the window block and append them to the paged cache.
+
+    k, v: [B][n][n_kv][hd], q: [B][n][n_q][hd], bf16 or fp32, any strides whose
+    rows are 16-byte aligned (slices of one packed projection, say).  pool: one
+    layer's pages; page_table int32 [B][max_pages]; seq_len, counts,
+    new_seq_len int32 [B]; pos int32 [B][n]; q_out [B*n][n_q][hd]; kv_win
+    [B][2][n_kv][Wp*hd]; k_norm, q_norm [hd]; error: int32 [1] that the
+    WEDLM_DEV_* bits are OR-ed into."""
+    import torch
+    if not k.is_cuda or k.dim() != 4:
+        raise _bad_arg("k must be a CUDA tensor [B][n][n_kv][hd]")
+    B, n, nkv, hd = k.shape
+    if B < 1 or n < 1 or nkv < 1:
+        raise _bad_arg("k has no rows")
+    code, i32, dt = _dtype_code(k), torch.int32, k.dtype
+    if v.shape != k.shape:
+        raise _bad_arg("v must have the shape of k")
+    if (q is None) != (q_out is None) or (q is None and q_norm is not None):
+        raise _bad_arg("q and q_out go together, and q_norm needs them")
+    nq = 0 if q is None else q.shape[2]
+    wp = (n + 15) // 16 * 16
+    args = AppendArgs(
+        batch=B, rows=n, n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, dtype=code,
+        max_pages_per_seq=page_table.shape[-1], num_pages=_pool_pages(pool, nkv, hd),
+        rms_eps=rms_eps, rope_theta=rope_theta, k=_take_rows("k", k, k, B, n),
+        v=_take_rows("v", v, k, B, n),
+        q_norm=_take("q_norm", q_norm, k, dt, (hd,), True),
+        k_norm=_take("k_norm", k_norm, k, dt, (hd,), True),
+        pos=_take("pos", pos, k, i32, (B, n), True),
+        counts=_take("counts", counts, k, i32, (B,), True),
+        seq_len=_take("seq_len", seq_len, k, i32, (B,)),
+        page_table=_take("page_table", page_table, k, i32, (B, page_table.shape[-1])),
+        kv_pool=_take("pool", pool, k, dt),
+        new_seq_len=_take("new_seq_len", new_seq_len, k, i32, (B,), True),
+        error=_take("error", error, k, i32, (1,), True))
+    if q is not None:
+        args.q = _take_rows("q", q, k, B, n)
+        args.q_out = _take("q_out", q_out, k, dt, (B * n, nq, hd))
+    if kv_win is not None:
+        args.kv_win = _take("kv_win", kv_win, k, dt, (B, 2, nkv, wp * hd))
+    rc = _launch(lib().wedlm_append_kv, args, k.device, stream)
+    if rc != OK:
+        raise WedlmError(rc, "wedlm_append_kv failed")
+
+
+def shared_prefix_attention(q, pool, shared_pages, page_table, seq_len, kv_win, o, error=None,
+                            workspace=None, stream=None):
+    """wedlm_shared_attention: window attention of a batch whose sequences share
+    the positions of `shared_pages` (int32 [S], or None), computed once for all.
+
+    q: [B*W][n_q][hd] (RoPE applied); pool: one layer's pages; page_table int32
+    [B][max_pages]; seq_len int32 [B], shared part included; kv_win
+    [B][2][n_kv][Wp*hd]; o: [B*W][n_q*hd], returned.  workspace: a byte tensor
+    of at least shared_prefix_workspace() bytes that no overlapping call uses;
+    by default one is taken from torch's allocator, on the call's stream."""
+    import torch
+    if not q.is_cuda or q.dim() != 3 or kv_win.dim() != 4 or seq_len.dim() != 1:
+        raise _bad_arg("q must be a CUDA tensor [B*W][n_q][hd], kv_win [B][2][n_kv][Wp*hd]")
+    (M, nq, hd), B, nkv = q.shape, seq_len.shape[0], kv_win.shape[2]
+    if B < 1 or M < 1 or M % B or nkv < 1:
+        raise _bad_arg("q must have W >= 1 rows for every sequence")
+    W, i32, dt, code = M // B, torch.int32, q.dtype, _dtype_code(q)
+    wp = (W + 15) // 16 * 16
+    S = 0 if shared_pages is None else shared_pages.shape[0]
+    args = SharedAttnArgs(
+        batch=B, window=W, n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, dtype=code,
+        n_shared_pages=S, max_pages_per_seq=page_table.shape[-1],
+        num_pages=_pool_pages(pool, nkv, hd), q=_take("q", q, q, dt),
+        kv_pool=_take("pool", pool, q, dt),
+        shared_pages=_take("shared_pages", shared_pages, q, i32, (S,), True) if S else None,
+        page_table=_take("page_table", page_table, q, i32, (B, page_table.shape[-1])),
+        seq_len=_take("seq_len", seq_len, q, i32, (B,)),
+        kv_win=_take("kv_win", kv_win, q, dt, (B, 2, nkv, wp * hd)),
+        o=_take("o", o, q, dt, (M, nq * hd)), error=_take("error", error, q, i32, (1,), True))
+    if q.device.index != torch.cuda.current_device():
+        with torch.cuda.device(q.device):
+            return _shared_prefix_attention(args, q, o, workspace, stream)
+    return _shared_prefix_attention(args, q, o, workspace, stream)
+
+
+def _shared_prefix_attention(args, q, o, workspace, stream):
+    import torch
+    L = lib()
+    if workspace is None:
+        need = L.wedlm_shared_attention_workspace(ctypes.byref(args))
+        if need == 0:
+            raise _bad_arg("sizes that wedlm_shared_attention does not take")
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:  # freed on return: its next user must come after this call on its stream
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise _bad_arg(f"workspace must be a contiguous tensor on {q.device}")
+    args.workspace = workspace.data_ptr()
+    args.workspace_bytes = workspace.numel() * workspace.element_size()
+    rc = L.wedlm_shared_attention(ctypes.byref(args), _stream_handle(stream))
+    if rc != OK:
+        raise WedlmError(rc, "wedlm_shared_attention failed")
+    return o
+
+
+def shared_prefix_workspace(batch, window, n_q_heads, n_kv_heads, head_dim, dtype,
+                            max_pages_per_seq, n_shared_pages=0):
+    """Bytes of workspace a shared_prefix_attention call of these sizes needs
+    (dtype: BF16 or FP32)."""
+    args = SharedAttnArgs(batch=batch, window=window, n_q_heads=n_q_heads, n_kv_heads=n_kv_heads,
+                          head_dim=head_dim, dtype=dtype, n_shared_pages=n_shared_pages,
+                          max_pages_per_seq=max_pages_per_seq, num_pages=1)
+    need = lib().wedlm_shared_attention_workspace(ctypes.byref(args))
+    if need == 0:
+        raise _bad_arg("sizes that wedlm_shared_attention does not take")
+    return need
 
 
 def selftest_bounded_wait(word, stream=None):

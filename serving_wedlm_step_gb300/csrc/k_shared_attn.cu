@@ -1,0 +1,109 @@
+// Shared-prefix window attention: argument checks, workspace and launches.
+#include <math.h>
+
+#include <algorithm>
+
+#include "shared_attn.cuh"
+
+namespace wedlm {
+namespace {
+
+constexpr int kSimtRowsPerUnit = 64;
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Sizes of a call: its split and the workspace's layout.  False for sizes the
+// kernels do not take.
+struct SharedPlan {
+  SharedArgs A{};
+  size_t off_part_p, off_ml_s, off_ml_p, off_units, bytes;
+};
+
+bool shared_plan(const wedlm_shared_attn_args& a, SharedPlan* P) {
+  if ((a.dtype != WEDLM_BF16 && a.dtype != WEDLM_FP32) ||
+      (a.head_dim != 64 && a.head_dim != 128) || a.batch < 1 || a.batch > kSharedMaxBatch ||
+      a.window < 1 || a.window > kMaxWindow || a.n_kv_heads < 1 || a.n_q_heads < a.n_kv_heads ||
+      a.n_q_heads % a.n_kv_heads || a.n_q_heads / a.n_kv_heads > 128 || a.n_kv_heads > 1024 ||
+      a.n_shared_pages < 0 || a.n_shared_pages > (1 << 26) || a.max_pages_per_seq < 1 ||
+      a.max_pages_per_seq > (1 << 26) || a.num_pages < 1)
+    return false;
+  SharedArgs& A = P->A;
+  A.B = a.batch;
+  A.W = a.window;
+  A.Wp = (a.window + kPageBlock - 1) / kPageBlock * kPageBlock;
+  A.G = a.n_q_heads / a.n_kv_heads;
+  A.nkv = a.n_kv_heads;
+  A.nsp = a.n_shared_pages;
+  A.max_pages = a.max_pages_per_seq;
+  A.num_pages = a.num_pages;
+  A.scale_log2 = (float)(1.4426950408889634 / sqrt((double)a.head_dim));
+  A.srows = std::min(kSimtRowsPerUnit, A.B * A.W * A.G);
+  A.prows = std::min(kSimtRowsPerUnit, A.W * A.G);
+  A.sblocks = (A.B * A.W * A.G + A.srows - 1) / A.srows;
+  A.pblocks = (A.W * A.G + A.prows - 1) / A.prows;
+  A.ucost = 1;
+  A.shared_cost = A.private_cost = A.min_share = 1;
+  const long long su = (long long)A.nkv * A.sblocks, pu = (long long)A.B * A.nkv * A.pblocks;
+  if (su + pu > (1 << 24)) return false;
+  const size_t ss = (size_t)su + kSharedMaxGrid, ps = (size_t)pu + kSharedMaxGrid;
+  size_t at = align256(ss * A.srows * a.head_dim * sizeof(float));
+  P->off_part_p = at;
+  at += align256(ps * A.prows * a.head_dim * sizeof(float));
+  P->off_ml_s = at;
+  at += align256(ss * A.srows * sizeof(float2));
+  P->off_ml_p = at;
+  at += align256(ps * A.prows * sizeof(float2));
+  P->off_units = at;
+  at += align256((size_t)(su + pu) * sizeof(int2));
+  P->bytes = at;
+  return true;
+}
+
+}  // namespace
+}  // namespace wedlm
+
+using namespace wedlm;
+
+extern "C" size_t wedlm_shared_attention_workspace(const wedlm_shared_attn_args* args) {
+  SharedPlan P;
+  return args && shared_plan(*args, &P) ? P.bytes : 0;
+}
+
+extern "C" int wedlm_shared_attention(const wedlm_shared_attn_args* a, void* stream) {
+  if (!a) return WEDLM_ERR_INVALID_ARG;
+  auto bad = [](const void* p, int align) {
+    return !p || (reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0;
+  };
+  SharedPlan P;
+  if (!shared_plan(*a, &P) || bad(a->q, 16) || bad(a->kv_pool, 16) || bad(a->kv_win, 16) ||
+      bad(a->o, 16) || bad(a->page_table, 4) || bad(a->seq_len, 4) || bad(a->workspace, 256) ||
+      (a->n_shared_pages && bad(a->shared_pages, 4)) || (a->error && bad(a->error, 4)))
+    return WEDLM_ERR_INVALID_ARG;
+  if (a->workspace_bytes < P.bytes) return WEDLM_ERR_CAPACITY;
+  SharedArgs& A = P.A;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return WEDLM_ERR_CUDA;
+  A.grid = std::min(sms, kSharedMaxGrid);  // one block per SM
+  A.q = a->q;
+  A.pool = a->kv_pool;
+  A.kv_win = a->kv_win;
+  A.shared = a->shared_pages;
+  A.page_table = a->page_table;
+  A.seq_len = a->seq_len;
+  A.o = a->o;
+  A.err = a->error;
+  char* ws = static_cast<char*>(a->workspace);
+  A.part_s = reinterpret_cast<float4*>(ws);
+  A.part_p = reinterpret_cast<float4*>(ws + P.off_part_p);
+  A.ml_s = reinterpret_cast<float2*>(ws + P.off_ml_s);
+  A.ml_p = reinterpret_cast<float2*>(ws + P.off_ml_p);
+  A.unit_blocks = reinterpret_cast<int2*>(ws + P.off_units);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool is_bf16 = a->dtype == WEDLM_BF16;
+  if (launch_shared_attention_simt(A, a->head_dim, is_bf16, st) != cudaSuccess ||
+      launch_shared_merge(A, a->head_dim, is_bf16, st) != cudaSuccess)
+    return WEDLM_ERR_CUDA;
+  return WEDLM_OK;
+}

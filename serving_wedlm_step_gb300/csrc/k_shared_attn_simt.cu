@@ -1,0 +1,291 @@
+// Shared-prefix window attention on the CUDA cores, and the merge of the
+// partials of either kernel.
+//
+// One pass over a segment's keys with the running maximum m and sum l of each
+// row, in log2 units:
+//   s = q k * log2(e)/sqrt(hd),  m' = max(m, max s),
+//   l = l 2^(m-m') + sum 2^(s-m'),  O = O 2^(m-m') + 2^(s-m') V
+// 64 rows x 128 keys per tile, 256 threads; a thread owns 4 rows x 8 keys of S
+// and 4 rows x 8 (4) dims of O, so a step of 4 dims (keys) does 128 FMAs on
+// 12 shared-memory vectors.  K, V and Q rows are padded by 4 floats: 8 lanes
+// that read 8 rows touch 32 different banks.
+#include "shared_attn.cuh"
+
+namespace wedlm {
+namespace {
+
+constexpr int kSimtRows = 64;
+constexpr int kSimtThreads = 256;
+constexpr int kPRow = kSharedTile + 4;
+
+template <int HD> constexpr int simt_smem_bytes() {
+  return ((kSimtRows + 2 * kSharedTile) * (HD + 4) + kSimtRows * kPRow) * (int)sizeof(float);
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedArgs A) {
+  constexpr int LD = HD + 4, ND = HD / 64;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;                        // [64][LD], scaled
+  float* Ks = Qs + kSimtRows * LD;       // [128][LD]
+  float* Vs = Ks + kSharedTile * LD;     // [128][LD]
+  float* Ps = Vs + kSharedTile * LD;     // [64][kPRow]
+  __shared__ long long s_w[kSharedMaxBatch + 1];
+  __shared__ int s_any;
+  pdl_wait();
+  pdl_trigger();
+  const SharedSplit S = shared_split(A, s_w, &s_any);
+  if ((int)blockIdx.x >= S.blocks) return;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int nq = A.nkv * A.G;
+  SharedWalk walk;
+  walk.init(S, blockIdx.x);
+  SharedSeg g;
+  while (walk.next(A, S, s_w, g)) {
+    const SeqSpan sp = g.b < 0 ? SeqSpan{0, 0} : seq_span(A, g.b, false);
+    const int n_own = g.b < 0 ? 0 : own_pages(sp);
+    const int own_keys = sp.len - sp.shared * kPageBlock;
+    const int pages = g.b < 0 ? A.nsp : n_own + A.Wp / kPageBlock;
+    const int urows = g.b < 0 ? A.srows : A.prows;
+    const int all_rows = (g.b < 0 ? A.B : 1) * A.W * A.G;
+    const int row0 = g.blk * urows, nrows = min(urows, all_rows - row0);
+    const int tok0 = g.b < 0 ? 0 : g.b * A.W;
+    const T* q = static_cast<const T*>(A.q);
+    __syncthreads();  // the previous segment is done with shared memory
+    for (int e = tid; e < kSimtRows * HD; e += kSimtThreads) {
+      const int r = e / HD, d = e % HD;
+      float v = 0.f;
+      if (r < nrows) {
+        const int row = row0 + r;
+        v = to_f(q[((size_t)(tok0 + row / A.G) * nq + g.kvh * A.G + row % A.G) * HD + d]);
+      }
+      Qs[r * LD + d] = v * A.scale_log2;
+    }
+    float m[4], l[4], o[4][4 * ND];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4 * ND; ++j) o[i][j] = 0.f;
+    }
+    for (int t = g.t0; t < g.t1; ++t) {
+      const int np = min(kSharedTilePages, pages - t * kSharedTilePages);
+      const int k0 = t * kSharedTile;
+      __syncthreads();
+      // stage the tile, row-major; what no row sees becomes zeros
+      constexpr int N = Vec16<T>::N, CH = kPageBlock * HD / N;
+      for (int e = tid; e < 2 * kSharedTilePages * CH; e += kSimtThreads) {
+        const int kv = e / (kSharedTilePages * CH), pg = e / CH % kSharedTilePages;
+        const int el = e % CH * N, tile = el / 64;
+        const int tok = tile / (HD / 8) * 8 + el % 64 / 8, d = tile % (HD / 8) * 8 + el % 8;
+        const int j = t * kSharedTilePages + pg, key = j * kPageBlock + tok;
+        Vec16<T> v;
+        v.raw = make_uint4(0, 0, 0, 0);
+        const bool seen = pg < np && (g.b < 0 || key < own_keys ||
+                                      (j >= n_own && key - n_own * kPageBlock < A.W));
+        if (seen) {
+          const T* src = unit_page<T>(A, g, sp, n_own, j, kv, HD);
+          if (src) v = ld16(src + el);
+        }
+        float* dst = (kv ? Vs : Ks) + (pg * kPageBlock + tok) * LD + d;
+#pragma unroll
+        for (int i = 0; i < N; ++i) dst[i] = v.get(i);
+      }
+      __syncthreads();
+      float s[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] = 0.f;
+#pragma unroll 2
+      for (int d = 0; d < HD; d += 4) {
+        float4 qv[4], kv4[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          qv[i] = *reinterpret_cast<const float4*>(Qs + (ty * 4 + i) * LD + d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          kv4[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * LD + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            s[i][j] = fmaf(qv[i].x, kv4[j].x, s[i][j]);
+            s[i][j] = fmaf(qv[i].y, kv4[j].y, s[i][j]);
+            s[i][j] = fmaf(qv[i].z, kv4[j].z, s[i][j]);
+            s[i][j] = fmaf(qv[i].w, kv4[j].w, s[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p_row = (row0 + ty * 4 + i) / A.G;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int key = k0 + tx + 16 * j;
+          bool ok = tx + 16 * j < np * kPageBlock;
+          if (g.b >= 0) {
+            const int w = key - n_own * kPageBlock;
+            ok = ok && (w < 0 ? key < own_keys : w < A.W && w <= p_row);
+          }
+          if (!ok) s[i][j] = -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1)
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float mn = fmaxf(m[i], mx);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float a = exp2f(m[i] - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float p = exp2f(s[i][j] - base);
+          sum += p;
+          Ps[(ty * 4 + i) * kPRow + tx + 16 * j] = p;
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        l[i] = l[i] * a + sum;
+        m[i] = mn;
+#pragma unroll
+        for (int j = 0; j < 4 * ND; ++j) o[i][j] *= a;
+      }
+      __syncwarp();  // a row's P is written and read by the same warp
+#pragma unroll 2
+      for (int k = 0; k < np * kPageBlock; k += 4) {
+        float4 pv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          pv[i] = *reinterpret_cast<const float4*>(Ps + (ty * 4 + i) * kPRow + k);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int j = 0; j < ND; ++j) {
+            const float4 v = *reinterpret_cast<const float4*>(Vs + (k + kk) * LD + tx * 4 + 64 * j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
+              o[i][4 * j] = fmaf(p, v.x, o[i][4 * j]);
+              o[i][4 * j + 1] = fmaf(p, v.y, o[i][4 * j + 1]);
+              o[i][4 * j + 2] = fmaf(p, v.z, o[i][4 * j + 2]);
+              o[i][4 * j + 3] = fmaf(p, v.w, o[i][4 * j + 3]);
+            }
+          }
+      }
+      __syncwarp();
+    }
+    if (tid == 0) record_unit(A, g);
+    const size_t slot = seg_slot(A, g.unit, blockIdx.x);
+    float4* po = (g.b < 0 ? A.part_s : A.part_p) + slot * (HD / 4) * urows;
+    float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + slot * urows;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      if (r >= nrows) continue;
+#pragma unroll
+      for (int j = 0; j < ND; ++j)
+        po[(size_t)(tx + 16 * j) * urows + r] =
+            make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
+      if (tx == 0) ml[r] = make_float2(m[i], l[i]);
+    }
+  }
+}
+
+// The merge: row r of kv head kvh takes the partials of its shared unit (when
+// its sequence takes part) and of its private unit, in slot order.
+// grid (ceil(rows/32), nkv), a warp per 32 dims, a lane per row.
+template <typename T, int HD>
+__global__ void __launch_bounds__(HD) shared_merge_kernel(SharedArgs A) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31, d40 = threadIdx.x / 32 * 8;
+  const int kvh = blockIdx.y, rows = A.B * A.W * A.G;
+  const int r = blockIdx.x * 32 + lane;
+  if (r >= rows) return;
+  const int tok = r / A.G, b = tok / A.W, pr = r - b * A.W * A.G;
+  float M = -INFINITY, ls = 0.f, acc[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+  for (int part = 0; part < 2; ++part) {
+    int unit, urows, idx;
+    const float4* po;
+    const float2* ml;
+    if (part == 0) {
+      if (!seq_span(A, b, false).shared) continue;
+      unit = kvh * A.sblocks + r / A.srows;
+      urows = A.srows;
+      idx = r % A.srows;
+      po = A.part_s;
+      ml = A.ml_s;
+    } else {
+      unit = A.nkv * A.sblocks + (b * A.nkv + kvh) * A.pblocks + pr / A.prows;
+      urows = A.prows;
+      idx = pr % A.prows;
+      po = A.part_p;
+      ml = A.ml_p;
+    }
+    const int2 blocks = A.unit_blocks[unit];
+    for (int c = blocks.x; c <= blocks.y; ++c) {
+      const size_t slot = seg_slot(A, unit, c);
+      const float2 s = ml[slot * urows + idx];
+      if (s.x == -INFINITY) continue;  // no key seen in this segment
+      const float4* src = po + (slot * (HD / 4) + d40) * urows + idx;
+      float4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = src[(size_t)j * urows];
+      const float Mn = fmaxf(M, s.x);
+      const float a = exp2f(M - Mn), w = exp2f(s.x - Mn);  // a = 0 while M is -inf
+      M = Mn;
+      ls = ls * a + s.y * w;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        acc[4 * j] = acc[4 * j] * a + v[j].x * w;
+        acc[4 * j + 1] = acc[4 * j + 1] * a + v[j].y * w;
+        acc[4 * j + 2] = acc[4 * j + 2] * a + v[j].z * w;
+        acc[4 * j + 3] = acc[4 * j + 3] * a + v[j].w * w;
+      }
+    }
+  }
+  const float inv = 1.f / ls;  // a window row sees itself: ls > 0
+  T* dst = static_cast<T*>(A.o) +
+           ((size_t)tok * A.nkv * A.G + kvh * A.G + r % A.G) * HD + d40 * 4;
+  constexpr int N = Vec16<T>::N;
+#pragma unroll
+  for (int j = 0; j < 32; j += N) {
+    Vec16<T> v;
+#pragma unroll
+    for (int k = 0; k < N; ++k) v.set(k, acc[j + k] * inv);
+    st16(dst + j, v);
+  }
+}
+
+template <typename T, int HD>
+cudaError_t launch_simt(const SharedArgs& A, cudaStream_t st) {
+  constexpr int smem = simt_smem_bytes<HD>();
+  const cudaError_t e = cudaFuncSetAttribute(shared_attn_simt_kernel<T, HD>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(shared_attn_simt_kernel<T, HD>, dim3(A.grid), dim3(kSimtThreads), smem, st, A);
+}
+
+template <typename T, int HD>
+cudaError_t launch_merge(const SharedArgs& A, cudaStream_t st) {
+  const int rows = A.B * A.W * A.G;
+  return launch_pdl(shared_merge_kernel<T, HD>, dim3((rows + 31) / 32, A.nkv), dim3(HD), 0, st, A);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_attention_simt(const SharedArgs& A, int hd, bool is_bf16,
+                                         cudaStream_t st) {
+  if (is_bf16) return hd == 128 ? launch_simt<bf16, 128>(A, st) : launch_simt<bf16, 64>(A, st);
+  return hd == 128 ? launch_simt<float, 128>(A, st) : launch_simt<float, 64>(A, st);
+}
+
+cudaError_t launch_shared_merge(const SharedArgs& A, int hd, bool is_bf16, cudaStream_t st) {
+  if (is_bf16) return hd == 128 ? launch_merge<bf16, 128>(A, st) : launch_merge<bf16, 64>(A, st);
+  return hd == 128 ? launch_merge<float, 128>(A, st) : launch_merge<float, 64>(A, st);
+}
+
+}  // namespace wedlm
