@@ -8,14 +8,13 @@
 namespace wedlm {
 namespace {
 
-constexpr int kSimtRowsPerUnit = 64;
-
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Sizes of a call: its split and the workspace's layout.  False for sizes the
 // kernels do not take.
 struct SharedPlan {
   SharedArgs A{};
+  int TPB;  // tokens per row block of the tensor-core kernel
   size_t off_part_p, off_ml_s, off_ml_p, off_units, bytes;
 };
 
@@ -37,12 +36,22 @@ bool shared_plan(const wedlm_shared_attn_args& a, SharedPlan* P) {
   A.max_pages = a.max_pages_per_seq;
   A.num_pages = a.num_pages;
   A.scale_log2 = (float)(1.4426950408889634 / sqrt((double)a.head_dim));
-  A.srows = std::min(kSimtRowsPerUnit, A.B * A.W * A.G);
-  A.prows = std::min(kSimtRowsPerUnit, A.W * A.G);
-  A.sblocks = (A.B * A.W * A.G + A.srows - 1) / A.srows;
-  A.pblocks = (A.W * A.G + A.prows - 1) / A.prows;
-  A.ucost = 1;
-  A.shared_cost = A.private_cost = A.min_share = 1;
+  const int rows = A.B * A.W * A.G, seq_rows = A.W * A.G;
+  P->TPB = 128 / A.G;
+  const int urows = a.dtype == WEDLM_BF16 ? 2 * P->TPB * A.G : kSimtRows;
+  A.srows = std::min(urows, rows);
+  A.prows = std::min(urows, seq_rows);
+  A.sblocks = (rows + A.srows - 1) / A.srows;
+  A.pblocks = (seq_rows + A.prows - 1) / A.prows;
+  if (a.dtype == WEDLM_BF16) {
+    A.ucost = 3;
+    A.shared_cost = A.B * A.W > P->TPB ? 5 : 4;
+    A.private_cost = A.W > P->TPB ? 5 : 4;
+    A.min_share = 8;
+  } else {
+    A.ucost = 1;
+    A.shared_cost = A.private_cost = A.min_share = 1;
+  }
   const long long su = (long long)A.nkv * A.sblocks, pu = (long long)A.B * A.nkv * A.pblocks;
   if (su + pu > (1 << 24)) return false;
   const size_t ss = (size_t)su + kSharedMaxGrid, ps = (size_t)pu + kSharedMaxGrid;
@@ -102,7 +111,8 @@ extern "C" int wedlm_shared_attention(const wedlm_shared_attn_args* a, void* str
   A.unit_blocks = reinterpret_cast<int2*>(ws + P.off_units);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool is_bf16 = a->dtype == WEDLM_BF16;
-  if (launch_shared_attention_simt(A, a->head_dim, is_bf16, st) != cudaSuccess ||
+  if ((is_bf16 ? launch_shared_attention_tc(A, a->head_dim, P.TPB, st)
+               : launch_shared_attention_simt(A, a->head_dim, st)) != cudaSuccess ||
       launch_shared_merge(A, a->head_dim, is_bf16, st) != cudaSuccess)
     return WEDLM_ERR_CUDA;
   return WEDLM_OK;

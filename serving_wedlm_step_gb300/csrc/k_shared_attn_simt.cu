@@ -14,7 +14,6 @@
 namespace wedlm {
 namespace {
 
-constexpr int kSimtRows = 64;
 constexpr int kSimtThreads = 256;
 constexpr int kPRow = kSharedTile + 4;
 
@@ -277,9 +276,7 @@ cudaError_t launch_merge(const SharedArgs& A, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_shared_attention_simt(const SharedArgs& A, int hd, bool is_bf16,
-                                         cudaStream_t st) {
-  if (is_bf16) return hd == 128 ? launch_simt<bf16, 128>(A, st) : launch_simt<bf16, 64>(A, st);
+cudaError_t launch_shared_attention_simt(const SharedArgs& A, int hd, cudaStream_t st) {
   return hd == 128 ? launch_simt<float, 128>(A, st) : launch_simt<float, 64>(A, st);
 }
 

@@ -1,0 +1,637 @@
+// Shared-prefix window attention on the 5th-generation tensor cores (bf16).
+//
+// A block (one per SM) holds two streams, A and B: 128 query rows each of Q, S,
+// P and O, one warpgroup of softmax each.  A unit (a range of query rows of one
+// kv head, see shared_attn.cuh) takes them in one of two ways:
+//   pair:  more than one row block (TPB = 128/G tokens, at most 128 rows): A
+//          takes the first, B the second, and both read every K/V tile, so a
+//          tile's 64 KB feed 256 rows;
+//   split: one row block: A takes the even key tiles, B the odd ones, and the
+//          two (m, l, O) are joined before they leave the block.
+// While one stream's softmax runs, the tensor core works for the other.
+//
+// One tile of one stream (128 keys):
+//   S = Q K^T   (tcgen05.mma, A = Q and B = K from shared memory) -> TMEM S
+//   P = 2^(S * scale - m), bf16, written over the first half of S (softmax)
+//   O += P V    (A = P from TMEM, B = V from shared memory)       -> TMEM O
+// P holds bf16 because the MMA takes both operands in one type; its rounding is
+// as large as that of the output.  The running maximum m is raised only when a
+// tile exceeds it by 2^8; until then the exponentials are taken against the
+// stale one, which the division by l (held in 32 bits, like m and O) undoes.
+//
+// TMEM (512 columns): S/P of A at 0, of B at 128, O of A at 256, of B at 384.
+// One thread issues every MMA, in the order A: P V, next S; B: P V, next S; the
+// tensor core runs them in that order, so S may follow P V into the columns that
+// P V reads.
+//
+// Warps (384 threads): 0-3 softmax of A (thread = row), 4-7 of B, 8 copies Q
+// (TMA) and K/V pages (4 KiB bulk copies in the 8x8-tile operand layout, a lane
+// per page) into a ring, 9 issues the MMAs; 10 and 11 only fill the warpgroup
+// whose registers the softmax warps take over (a row's 128 scores stay in
+// registers): 256 x 208 + 128 x 88 = 384 x 168, what the block was launched with.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "shared_attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace wedlm {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRing = 4;                 // K/V tiles in shared memory
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
+constexpr float kRaise = 8.f;            // log2 units
+
+template <int N> __device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int HD> struct Cfg {
+  static constexpr uint32_t kPage = kPageBlock * HD * 2;
+  static constexpr uint32_t kTileBytes = kSharedTile * HD * 2;
+  static constexpr uint32_t kQBytes = 128 * HD * 2;
+  static constexpr uint32_t kSmem = 2 * kQBytes + kRing * kTileBytes + 128;
+};
+
+// what a segment needs beyond its place in the split
+struct Seg : SharedSeg {
+  bool pair;
+  int n, nB;              // tiles of the segment (of stream A in pair mode), of B
+  SeqSpan sp;
+  int n_own, own_keys, pages;
+  int tok0, ntok;         // first query token of the unit, tokens in it
+};
+
+__device__ __forceinline__ void expand(const SharedArgs& A, int TPB, Seg& g) {
+  const int n = g.t1 - g.t0;
+  if (g.b < 0) {
+    g.tok0 = g.blk * 2 * TPB;
+    g.ntok = min(2 * TPB, A.B * A.W - g.tok0);
+    g.sp = SeqSpan{0, 0};
+    g.n_own = g.own_keys = 0;
+    g.pages = A.nsp;
+  } else {
+    const int w0 = g.blk * 2 * TPB;
+    g.tok0 = g.b * A.W + w0;
+    g.ntok = min(2 * TPB, A.W - w0);
+    g.sp = seq_span(A, g.b, false);
+    g.n_own = own_pages(g.sp);
+    g.own_keys = g.sp.len - g.sp.shared * kPageBlock;
+    g.pages = g.n_own + A.Wp / kPageBlock;
+  }
+  g.pair = g.ntok > TPB;
+  g.n = g.pair ? n : (n + 1) / 2;
+  g.nB = g.pair ? n : n / 2;
+}
+__device__ __forceinline__ int seg_tile(const Seg& g, int x, int j) {
+  return g.t0 + (g.pair ? j : 2 * j + x);
+}
+__device__ __forceinline__ int tile_pages(const Seg& g, int t) {
+  return min(kSharedTilePages, g.pages - t * kSharedTilePages);
+}
+
+// The order in which K/V tiles are used; the copier and the MMA issuer both
+// follow it.  on_s(x, seg, j) / on_pv(x, seg, j): tile j of stream x; false ends
+// the walk.
+template <typename OnS, typename OnPV>
+__device__ __forceinline__ void run_tiles(const SharedArgs& A, const SharedSplit& S,
+                                          const long long* s_w, int TPB, OnS on_s, OnPV on_pv) {
+  SharedWalk walk;
+  walk.init(S, blockIdx.x);
+  Seg cur, nxt;
+  if (!walk.next(A, S, s_w, cur)) return;
+  expand(A, TPB, cur);
+  if (!on_s(0, cur, 0) || (cur.nB > 0 && !on_s(1, cur, 0))) return;
+  while (true) {
+    const bool more = walk.next(A, S, s_w, nxt);
+    if (more) expand(A, TPB, nxt);
+#pragma unroll 1
+    for (int j = 0; j < cur.n; ++j) {
+      const bool last = j + 1 == cur.n;
+      if (!on_pv(0, cur, j)) return;
+      if (!last) {
+        if (!on_s(0, cur, j + 1)) return;
+      } else if (more) {
+        if (!on_s(0, nxt, 0)) return;
+      }
+      if (j < cur.nB && !on_pv(1, cur, j)) return;
+      if (!last) {
+        if (j + 1 < cur.nB && !on_s(1, cur, j + 1)) return;
+      } else if (more && nxt.nB > 0) {
+        if (!on_s(1, nxt, 0)) return;
+      }
+    }
+    if (!more) return;
+    cur = nxt;
+  }
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc]: A's lane is its row, each 32-bit column
+// two consecutive K elements
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void load_q_box(void* dst, const CUtensorMap* m, uint64_t* bar, int c0,
+                                           int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+#define R8(a, i) "=f"(a[i]), "=f"(a[i + 1]), "=f"(a[i + 2]), "=f"(a[i + 3]), "=f"(a[i + 4]), \
+                 "=f"(a[i + 5]), "=f"(a[i + 6]), "=f"(a[i + 7])
+// 32 lanes x 64 columns, complete on return (load and wait in one statement, so
+// that no use can move in between)
+__device__ __forceinline__ void ld64(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, "
+      "[%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : R8(v, 0), R8(v, 8), R8(v, 16), R8(v, 24), R8(v, 32), R8(v, 40), R8(v, 48), R8(v, 56)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+      "[%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      : R8(v, 0), R8(v, 8), R8(v, 16), R8(v, 24)
+      : "r"(taddr)
+      : "memory");
+}
+#undef R8
+#define W8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), \
+                 "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+          taddr),
+      W8(r, 0), W8(r, 8), W8(r, 16), W8(r, 24)
+      : "memory");
+}
+#undef W8
+__device__ __forceinline__ void wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int TPB) {
+  using C = Cfg<HD>;
+  extern __shared__ uint8_t dsm[];
+  __shared__ __align__(8) uint64_t kv_full[kRing], kv_empty[kRing], q_full[2], q_empty[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], fin;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_any, s_issued, s_taken, s_qissued[2], s_qtaken[2];
+  __shared__ float2 s_ml[2][128];
+  __shared__ long long s_w[kSharedMaxBatch + 1];
+
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 127) &
+                                             ~static_cast<uintptr_t>(127));
+  uint8_t* ring = base + 2 * C::kQBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = A.G;
+
+  pdl_wait();
+  pdl_trigger();
+  const SharedSplit S = shared_split(A, s_w, &s_any);
+  if ((int)blockIdx.x >= S.blocks) return;  // the whole block
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&pv_done[x], 1);
+      s_qissued[x] = s_qtaken[x] = 0;
+    }
+    mbar_init(&fin, 1);
+    s_abort = s_issued = s_taken = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s_tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  volatile int* abort = &s_abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (mbar_wait(bar, parity, A.err)) return true;
+    *abort = 1;
+    return false;
+  };
+
+  if (warp >= 8) {
+    regs_down<88>();
+    if (warp == 8) {
+    // ---------------- copier ----------------
+    if (lane == 0) tma_prefetch_desc(&mq);
+    const uint64_t keep = l2_evict_last_policy(), once = l2_evict_first_policy();
+    int st = 0;
+    uint32_t ph = 0;
+    int issued = 0, flip = 0, nq[2] = {0, 0};
+    // this lane's page of the next K and V tile
+    const bf16* next[2] = {nullptr, nullptr};
+    auto page_of = [&](const Seg& g, int t, int kv) -> const bf16* {
+      const int j = t * kSharedTilePages + lane;
+      return lane < kSharedTilePages && t < g.t1 && j < g.pages
+                 ? unit_page<bf16>(A, g, g.sp, g.n_own, j, kv, HD)
+                 : nullptr;
+    };
+    auto load_tile = [&](const Seg& g, int t, int kv) -> bool {
+      const int np = tile_pages(g, t);
+      const bf16* src = next[kv];
+      next[kv] = page_of(g, t + 1, kv);
+      if (!wait(&kv_empty[st], ph ^ 1u)) return false;
+      uint8_t* dst = ring + st * C::kTileBytes;
+      const unsigned missing = __ballot_sync(0xffffffffu, lane < np && !src);
+      if (missing) {  // page ids out of range read as zeros
+        for (int p = 0; p < np; ++p)
+          if (missing >> p & 1)
+            for (int e = lane; e < (int)C::kPage / 16; e += 32)
+              reinterpret_cast<uint4*>(dst + p * C::kPage)[e] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0)
+        mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(np - __popc(missing)) * C::kPage);
+      __syncwarp();
+      if (lane < np && src)
+        bulk_load(dst + lane * C::kPage, src, C::kPage, &kv_full[st], g.b < 0 ? keep : once);
+      if (lane == 0) s_issued = ++issued;
+      if (++st == kRing) {
+        st = 0;
+        ph ^= 1u;
+      }
+      return true;
+    };
+    auto load_q = [&](const Seg& g, int buf, int tok) -> bool {
+      if (!wait(&q_empty[buf], (uint32_t)(nq[buf] & 1) ^ 1u)) return false;
+      ++nq[buf];
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[buf], (uint32_t)(min(TPB, A.B * A.W) * G) * HD * 2);
+#pragma unroll 1
+        for (int c = 0; c < HD / 8; ++c)
+          load_q_box(base + buf * C::kQBytes + c * 2048, &mq, &q_full[buf], 8 * c, g.kvh * G, tok);
+        s_qissued[buf] = nq[buf];
+      }
+      return true;
+    };
+    run_tiles(
+        A, S, s_w, TPB,
+        [&](int x, const Seg& g, int j) -> bool {
+          if (j == 0) {
+            if (x == 0) next[0] = page_of(g, g.t0, 0);
+            if (g.pair) {
+              if (!load_q(g, x, g.tok0 + x * TPB)) return false;
+            } else if (x == 0) {
+              if (!load_q(g, flip, g.tok0)) return false;
+              flip ^= 1;
+            }
+          }
+          return (g.pair && x == 1) || load_tile(g, seg_tile(g, x, j), 0);
+        },
+        [&](int x, const Seg& g, int j) -> bool {
+          if (j == 0 && x == 0) next[1] = page_of(g, g.t0, 1);
+          return (g.pair && x == 1) || load_tile(g, seg_tile(g, x, j), 1);
+        });
+    } else if (warp == 9) {
+    // ---------------- MMA issuer ----------------
+    // Q: 8-dim groups 2048 B apart, 8-row groups 128 B; K: 128 B and HD*16 B
+    // (K-major); V: 8-token groups HD*16 B apart, 8-dim groups 128 B (MN-major)
+    const uint64_t dq0 = sdesc_noswz(smem_u32(base), 2048, 128);
+    const uint64_t dk0 = sdesc_noswz(smem_u32(ring), 128, HD * 16);
+    const uint64_t dv0 = sdesc_noswz(smem_u32(ring), HD * 16, 128);
+    const uint32_t idPV = idesc_bf16_m128(HD) | (1u << 16);
+    int st = 0, kst = 0, vst = 0, taken = 0, flip = 0, nq[2] = {0, 0}, qbuf = 0;
+    uint32_t ph = 0, pph[2] = {0, 0};
+    auto take = [&](int& slot) -> bool {
+      if (!wait(&kv_full[st], ph)) return false;
+      slot = st;
+      if (lane == 0) s_taken = ++taken;
+      if (++st == kRing) {
+        st = 0;
+        ph ^= 1u;
+      }
+      return true;
+    };
+    auto take_q = [&](int buf) -> bool {
+      if (!wait(&q_full[buf], (uint32_t)(nq[buf] & 1))) return false;
+      ++nq[buf];
+      if (lane == 0) s_qtaken[buf] = nq[buf];
+      return true;
+    };
+    run_tiles(
+        A, S, s_w, TPB,
+        [&](int x, const Seg& g, int j) -> bool {
+          if (j == 0) {
+            if (g.pair) {
+              if (!take_q(x)) return false;
+            } else if (x == 0) {
+              qbuf = flip;
+              flip ^= 1;
+              if (!take_q(qbuf)) return false;
+            }
+          }
+          if (!(g.pair && x == 1) && !take(kst)) return false;
+          if (lane == 0) {
+            tc_fence_after();
+            const int buf = g.pair ? x : qbuf;
+            const uint64_t dq = dq0 + (uint64_t)(buf * C::kQBytes >> 4);
+            const uint64_t dk = dk0 + (uint64_t)(kst * C::kTileBytes >> 4);
+            const uint32_t id =
+                idesc_bf16_m128(tile_pages(g, seg_tile(g, x, j)) * kPageBlock);
+            const uint32_t d = tmem + kColS + (uint32_t)(x * 128);
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)  // 16 dims: two 8-dim groups
+              tc_mma_f16(d, dq + k * 256, dk + k * 16, id, k ? 1u : 0u);
+            tc_commit(&s_full[x]);
+            if (!g.pair || x == 1) tc_commit(&kv_empty[kst]);
+            const int nx = x ? g.nB : g.n;
+            if (g.pair ? j + 1 == nx : seg_tile(g, x, j) + 1 == g.t1) tc_commit(&q_empty[buf]);
+          }
+          __syncwarp();
+          return true;
+        },
+        [&](int x, const Seg& g, int j) -> bool {
+          const int t = seg_tile(g, x, j), np = tile_pages(g, t);
+          if (!(g.pair && x == 1)) {
+            if (!take(vst)) return false;
+            // V rows that no query sees (the tails of the last cached page and of
+            // the window) become zeros: 0 * NaN would reach every row
+            const int c_own = g.own_keys - t * kSharedTile;        // cached keys in this tile
+            const int c_win = g.n_own * kPageBlock - t * kSharedTile + A.W;  // window end
+            if (g.b >= 0 && ((c_own > 0 && c_own < kSharedTile && (c_own & 15)) ||
+                             (c_win > 0 && c_win < kSharedTile && (c_win & 15)))) {
+              for (int part = 0; part < 2; ++part) {
+                const int c = part ? c_win : c_own;
+                if (c <= 0 || c >= kSharedTile || !(c & 15)) continue;
+                const int rows = 16 - (c & 15);
+                for (int e = lane; e < rows * (HD / 8); e += 32)
+                  *reinterpret_cast<uint4*>(ring + vst * C::kTileBytes +
+                                            2 * ((c >> 4) * kPageBlock * HD +
+                                                 tile_off((c & 15) + e % rows, e / rows * 8, HD))) =
+                      make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          if (!wait(&p_full[x], pph[x])) return false;
+          pph[x] ^= 1u;
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t dv = dv0 + (uint64_t)(vst * C::kTileBytes >> 4);
+            const uint32_t d = tmem + kColO + (uint32_t)(x * 128);
+            const uint32_t p = tmem + kColS + (uint32_t)(x * 128);
+#pragma unroll
+            for (int k = 0; k < kSharedTilePages; ++k)  // 16 keys: 8 columns of P
+              if (k < np) mma_ts(d, p + k * 8, dv + k * (HD * 2), idPV, (j || k) ? 1u : 0u);
+            tc_commit(&pv_done[x]);
+            if (!g.pair || x == 1) tc_commit(&kv_empty[vst]);
+          }
+          __syncwarp();
+          return true;
+        });
+    // every MMA has completed before TMEM is freed
+    if (lane == 0) {
+      tc_commit(&fin);
+      mbar_wait(&fin, 0, A.err);
+    }
+    }
+  } else {
+    // ---------------- softmax ----------------
+    regs_up<208>();
+    const int x = warp >> 2;                       // stream
+    const int r = threadIdx.x & 127;               // row of the stream's row block
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + lane_off + kColS + (uint32_t)(x * 128);
+    const uint32_t tO = tmem + lane_off + kColO + (uint32_t)(x * 128);
+    const float sc = A.scale_log2;
+    uint32_t sph = 0, dph = 0;  // phases of s_full and of pv_done
+    auto both = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    SharedWalk walk;
+    walk.init(S, blockIdx.x);
+    Seg g;
+    while (walk.next(A, S, s_w, g)) {
+      expand(A, TPB, g);
+      const int nx = x ? g.nB : g.n;
+      // token of this row within the unit, its window row
+      const int utok = (g.pair ? x * TPB : 0) + r / G;
+      const int p_row = g.b < 0 ? 0 : g.blk * 2 * TPB + utok;
+      const bool valid = r < TPB * G && utok < g.ntok;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nx; ++j) {
+        const int t = seg_tile(g, x, j), np = tile_pages(g, t);
+        wait(&s_full[x], sph);
+        sph ^= 1u;
+        tc_fence_after();
+        float v[128];
+        ld64(tS, v);
+        ld64(tS + 64, v + 64);
+        // a tile of visible keys needs no mask
+        if (np < kSharedTilePages || (g.b >= 0 && (t + 1) * kSharedTile > g.own_keys)) {
+          const int c_own = g.b < 0 ? np * kPageBlock : g.own_keys - t * kSharedTile;
+          const int c_win = g.n_own * kPageBlock - t * kSharedTile;
+          const int c_end = g.b < 0 ? 0 : c_win + p_row + 1;  // window keys up to this row
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (!(c < c_own || (c >= c_win && c < c_end && c < np * kPageBlock))) v[c] = -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mx[k] = fmaxf(v[k], v[k + 4]);
+#pragma unroll
+          for (int c = 8; c < 128; c += 8)
+            mx[k] = fmaxf(mx[k], fmaxf(v[c + k], v[c + k + 4]));
+        }
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const bool raise = mt > m + kRaise;
+        if (__any_sync(0xffffffffu, raise)) {  // TMEM accesses are warp-wide
+          if (j > 0) {
+            const float a = !raise ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - mt);
+            wait(&pv_done[x], dph ^ 1u);  // P V of the tile before is in O
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < HD; c += 32) {
+              float o[32];
+              uint32_t u[32];
+              ld32(tO + c, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * a);
+              st32(tO + c, u);
+            }
+            l *= a;
+          }
+          if (raise) m = mt;
+        }
+        const float nm = m == -INFINITY ? 0.f : -m;
+        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float p0 = ex2_approx(fmaf(v[64 * h + c], sc, nm));
+            const float p1 = ex2_approx(fmaf(v[64 * h + c + 1], sc, nm));
+            ps[(c >> 1) & 3] += p0 + p1;
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+            pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          st32(tS + 32 * h, pk);
+        }
+        l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+        dph ^= 1u;
+      }
+      // the segment's partial: O once its last P V is done
+      if (nx > 0) wait(&pv_done[x], dph ^ 1u);
+      tc_fence_after();
+      const int urows = g.b < 0 ? A.srows : A.prows;
+      const size_t slot = seg_slot(A, g.unit, blockIdx.x);
+      float4* po = (g.b < 0 ? A.part_s : A.part_p) + slot * (HD / 4) * urows;
+      float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + slot * urows;
+      if (threadIdx.x == 0) record_unit(A, g);
+      if (g.pair) {
+        const int row = x * TPB * G + r;
+#pragma unroll
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          ld32(tO + c, o);
+          if (valid)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              po[(size_t)(c / 4 + k) * urows + row] =
+                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+        if (valid) ml[row] = make_float2(m, l);
+        tc_fence_before();
+      } else {
+        // join A and B: each warpgroup takes half of the dims of both
+        s_ml[x][r] = make_float2(m, l);
+        tc_fence_before();
+        both();
+        tc_fence_after();
+        const float2 o_ml = s_ml[x ^ 1][r];
+        const float M = fmaxf(m, o_ml.x);
+        const float am = m == -INFINITY ? 0.f : ex2_approx(m - M);
+        const float ao = o_ml.x == -INFINITY ? 0.f : ex2_approx(o_ml.x - M);
+        const float fa = x ? ao : am, fb = x ? am : ao;  // factors of A's and B's O
+        const uint32_t t0 = tmem + lane_off + kColO + (uint32_t)(x * HD / 2);
+#pragma unroll
+        for (int c = 0; c < HD / 2; c += 32) {
+          float o[32];
+          ld32(t0 + c, o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] *= fa;
+          if (g.nB > 0) {  // else B's O holds nothing of this segment
+            float ob[32];
+            ld32(t0 + 128 + c, ob);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = fmaf(ob[k], fb, o[k]);
+          }
+          if (valid)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              po[(size_t)((x * HD / 2 + c) / 4 + k) * urows + r] =
+                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+        if (valid && x == 0) ml[r] = make_float2(M, l * am + o_ml.y * ao);
+        tc_fence_before();
+        both();  // O and s_ml may be written again
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (s_abort && threadIdx.x == 256) {
+    // a wait expired: let the copies still in flight land (bounded)
+    for (int i = s_taken; i < s_issued; ++i)
+      mbar_wait(&kv_full[i % kRing], (uint32_t)(i / kRing) & 1u, A.err);
+    for (int x = 0; x < 2; ++x)
+      for (int i = s_qtaken[x]; i < s_qissued[x]; ++i)
+        mbar_wait(&q_full[x], (uint32_t)i & 1u, A.err);
+  }
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static std::atomic<void*> cached{nullptr};
+  void* p = cached.load(std::memory_order_acquire);
+  if (!p) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    cached.store(p, std::memory_order_release);
+  }
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+}
+
+template <int HD>
+cudaError_t launch(const SharedArgs& A, int TPB, cudaStream_t st) {
+  const auto enc = encoder();
+  if (!enc) return cudaErrorNotSupported;
+  // q as {dim, head, token}: a box of 8 dims, G heads and TPB tokens is one 8-dim
+  // group of a row block, rows token * G + g
+  CUtensorMap mq;
+  const cuuint64_t nq = (cuuint64_t)A.nkv * A.G;
+  cuuint64_t dims[3] = {HD, nq, (cuuint64_t)A.B * A.W};
+  cuuint64_t strides[2] = {HD * 2, nq * HD * 2};
+  cuuint32_t box[3] = {8, (cuuint32_t)A.G, (cuuint32_t)std::min(TPB, A.B * A.W)};
+  cuuint32_t one[3] = {1, 1, 1};
+  if (enc(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(A.q), dims, strides, box, one,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(shared_attn_tc_kernel<HD>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)Cfg<HD>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(shared_attn_tc_kernel<HD>, dim3(A.grid), dim3(kThreads), Cfg<HD>::kSmem, st, mq,
+                    A, TPB);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_attention_tc(const SharedArgs& A, int hd, int TPB, cudaStream_t st) {
+  return hd == 128 ? launch<128>(A, TPB, st) : launch<64>(A, TPB, st);
+}
+
+}  // namespace wedlm

@@ -204,8 +204,11 @@ __device__ __forceinline__ const T* unit_page(const SharedArgs& A, const SharedS
   return static_cast<const T*>(A.pool) + (((size_t)id * 2 + kv) * A.nkv + g.kvh) * blockn;
 }
 
-cudaError_t launch_shared_attention_simt(const SharedArgs& A, int hd, bool is_bf16,
-                                         cudaStream_t st);
+// fp32: urows query rows per unit, whatever tokens they belong to
+constexpr int kSimtRows = 64;
+cudaError_t launch_shared_attention_simt(const SharedArgs& A, int hd, cudaStream_t st);
+// bf16: units of 2 * TPB tokens, TPB = 128 / G
+cudaError_t launch_shared_attention_tc(const SharedArgs& A, int hd, int TPB, cudaStream_t st);
 cudaError_t launch_shared_merge(const SharedArgs& A, int hd, bool is_bf16, cudaStream_t st);
 
 }  // namespace wedlm
