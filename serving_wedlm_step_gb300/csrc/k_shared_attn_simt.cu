@@ -29,19 +29,27 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
   float* Ks = Qs + kSimtRows * LD;       // [128][LD]
   float* Vs = Ks + kSharedTile * LD;     // [128][LD]
   float* Ps = Vs + kSharedTile * LD;     // [64][kPRow]
-  __shared__ long long s_w[kSharedMaxBatch + 1];
-  __shared__ int s_any;
+  __shared__ SharedSeg s_seg;
+  __shared__ bool s_more;
   pdl_wait();
   pdl_trigger();
-  const SharedSplit S = shared_split(A, s_w, &s_any);
-  if ((int)blockIdx.x >= S.blocks) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int nq = A.nkv * A.G;
   SharedWalk walk;
-  walk.init(S, blockIdx.x);
-  SharedSeg g;
-  while (walk.next(A, S, s_w, g)) {
-    const SeqSpan sp = g.b < 0 ? SeqSpan{0, 0} : seq_span(A, g.b, false);
+  if (tid < 32) walk.init(A);
+  while (true) {
+    if (tid < 32) {
+      SharedSeg next;
+      const bool more = walk.next(A, next);
+      if (tid == 0) {
+        s_seg = next;
+        s_more = more;
+      }
+    }
+    __syncthreads();  // also: the previous segment is done with shared memory
+    if (!s_more) break;
+    const SharedSeg g = s_seg;
+    const SeqSpan sp = g.sp;
     const int n_own = g.b < 0 ? 0 : own_pages(sp);
     const int own_keys = sp.len - sp.shared * kPageBlock;
     const int pages = g.b < 0 ? A.nsp : n_own + A.Wp / kPageBlock;
@@ -50,7 +58,6 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
     const int row0 = g.blk * urows, nrows = min(urows, all_rows - row0);
     const int tok0 = g.b < 0 ? 0 : g.b * A.W;
     const T* q = static_cast<const T*>(A.q);
-    __syncthreads();  // the previous segment is done with shared memory
     for (int e = tid; e < kSimtRows * HD; e += kSimtThreads) {
       const int r = e / HD, d = e % HD;
       float v = 0.f;
@@ -84,8 +91,15 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
         const bool seen = pg < np && (g.b < 0 || key < own_keys ||
                                       (j >= n_own && key - n_own * kPageBlock < A.W));
         if (seen) {
-          const T* src = unit_page<T>(A, g, sp, n_own, j, kv, HD);
-          if (src) v = ld16(src + el);
+          if (g.b >= 0 && j >= n_own) {
+            v = ld16(window_block<T>(A, g.b, j - n_own, kv, g.kvh, HD) + el);
+          } else {
+            const int id = own_page_id(A, g.b, sp.shared, j);
+            if (id >= 0 && id < A.num_pages)
+              v = ld16(cached_block<T>(A, id, kv, g.kvh, HD) + el);
+            else
+              set_err(A.err, WEDLM_DEV_BAD_PAGE);
+          }
         }
         float* dst = (kv ? Vs : Ks) + (pg * kPageBlock + tok) * LD + d;
 #pragma unroll
@@ -177,7 +191,7 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
     }
     if (tid == 0) record_unit(A, g);
     const size_t slot = seg_slot(A, g.unit, blockIdx.x);
-    float4* po = (g.b < 0 ? A.part_s : A.part_p) + slot * (HD / 4) * urows;
+    float* po = (g.b < 0 ? A.part_s : A.part_p) + slot * urows * HD;
     float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + slot * urows;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -185,78 +199,93 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
       if (r >= nrows) continue;
 #pragma unroll
       for (int j = 0; j < ND; ++j)
-        po[(size_t)(tx + 16 * j) * urows + r] =
+        *reinterpret_cast<float4*>(po + (size_t)r * HD + tx * 4 + 64 * j) =
             make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
       if (tx == 0) ml[r] = make_float2(m[i], l[i]);
     }
   }
 }
 
-// The merge: row r of kv head kvh takes the partials of its shared unit (when
-// its sequence takes part) and of its private unit, in slot order.
-// grid (ceil(rows/32), nkv), a warp per 32 dims, a lane per row.
+// The merge: row r of kv head kvh joins the partials of its shared unit (when
+// its sequence takes part) and of its private unit, in slot order.  A warp per
+// row, HD/32 dims a lane: first the weights, 2^(m_i - M) / sum, of up to 32
+// partials at a time (a lane each), then their O, eight loads in flight.
+constexpr int kMergeWarps = 4;
 template <typename T, int HD>
-__global__ void __launch_bounds__(HD) shared_merge_kernel(SharedArgs A) {
+__global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(SharedArgs A) {
+  constexpr int N = HD / 32;
   pdl_wait();
-  const int lane = threadIdx.x & 31, d40 = threadIdx.x / 32 * 8;
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
   const int kvh = blockIdx.y, rows = A.B * A.W * A.G;
-  const int r = blockIdx.x * 32 + lane;
+  const int r = blockIdx.x * kMergeWarps + threadIdx.x / 32;
   if (r >= rows) return;
   const int tok = r / A.G, b = tok / A.W, pr = r - b * A.W * A.G;
-  float M = -INFINITY, ls = 0.f, acc[32];
+  const int us = kvh * A.sblocks + r / A.srows, is = r % A.srows;
+  const int up = A.nkv * A.sblocks + (b * A.nkv + kvh) * A.pblocks + pr / A.prows;
+  const int ip = pr % A.prows;
+  const int2 bs = A.unit_blocks[us], bp = A.unit_blocks[up];
+  const int ns = seq_span(A, b, false).shared ? bs.y - bs.x + 1 : 0;
+  const int n = ns + bp.y - bp.x + 1;
+  float M = -INFINITY, l = 0.f, acc[N];
 #pragma unroll
-  for (int j = 0; j < 32; ++j) acc[j] = 0.f;
-  for (int part = 0; part < 2; ++part) {
-    int unit, urows, idx;
-    const float4* po;
-    const float2* ml;
-    if (part == 0) {
-      if (!seq_span(A, b, false).shared) continue;
-      unit = kvh * A.sblocks + r / A.srows;
-      urows = A.srows;
-      idx = r % A.srows;
-      po = A.part_s;
-      ml = A.ml_s;
-    } else {
-      unit = A.nkv * A.sblocks + (b * A.nkv + kvh) * A.pblocks + pr / A.prows;
-      urows = A.prows;
-      idx = pr % A.prows;
-      po = A.part_p;
-      ml = A.ml_p;
+  for (int k = 0; k < N; ++k) acc[k] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    size_t off = 0;  // of partial i's row
+    if (i < n) {
+      off = i < ns ? (size_t)seg_slot(A, us, bs.x + i) * A.srows + is
+                   : (size_t)seg_slot(A, up, bp.x + i - ns) * A.prows + ip;
+      ml = (i < ns ? A.ml_s : A.ml_p)[off];
     }
-    const int2 blocks = A.unit_blocks[unit];
-    for (int c = blocks.x; c <= blocks.y; ++c) {
-      const size_t slot = seg_slot(A, unit, c);
-      const float2 s = ml[slot * urows + idx];
-      if (s.x == -INFINITY) continue;  // no key seen in this segment
-      const float4* src = po + (slot * (HD / 4) + d40) * urows + idx;
-      float4 v[8];
+    const float Mn = fmaxf(M, warp_max(ml.x));
+    if (Mn == -INFINITY) continue;
+    const float a = exp2f(M - Mn), w = exp2f(ml.x - Mn);  // 0 for -inf
+    M = Mn;
+    // a partial without keys (m = -inf) holds no O
+    l = l * a + warp_sum(ml.x == -INFINITY ? 0.f : ml.y * w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = src[(size_t)j * urows];
-      const float Mn = fmaxf(M, s.x);
-      const float a = exp2f(M - Mn), w = exp2f(s.x - Mn);  // a = 0 while M is -inf
-      M = Mn;
-      ls = ls * a + s.y * w;
+    for (int k = 0; k < N; ++k) acc[k] *= a;
+    const unsigned live = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
+    for (int j0 = 0; j0 < 32 && i0 + j0 < n; j0 += 8) {
+      float v[8][N], wj[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        acc[4 * j] = acc[4 * j] * a + v[j].x * w;
-        acc[4 * j + 1] = acc[4 * j + 1] * a + v[j].y * w;
-        acc[4 * j + 2] = acc[4 * j + 2] * a + v[j].z * w;
-        acc[4 * j + 3] = acc[4 * j + 3] * a + v[j].w * w;
+        const size_t o = __shfl_sync(0xffffffffu, off, j0 + j);
+        wj[j] = __shfl_sync(0xffffffffu, w, j0 + j);
+        const float* src = (i0 + j0 + j < ns ? A.part_s : A.part_p) + o * HD + lane * N;
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[j][k] = 0.f;
+        if (live >> (j0 + j) & 1) {
+          if constexpr (N == 4) {
+            const float4 t = *reinterpret_cast<const float4*>(src);
+            v[j][0] = t.x; v[j][1] = t.y; v[j][2] = t.z; v[j][3] = t.w;
+          } else {
+            const float2 t = *reinterpret_cast<const float2*>(src);
+            v[j][0] = t.x; v[j][1] = t.y;
+          }
+        } else {
+          wj[j] = 0.f;
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int k = 0; k < N; ++k) acc[k] = fmaf(v[j][k], wj[j], acc[k]);
     }
   }
-  const float inv = 1.f / ls;  // a window row sees itself: ls > 0
-  T* dst = static_cast<T*>(A.o) +
-           ((size_t)tok * A.nkv * A.G + kvh * A.G + r % A.G) * HD + d40 * 4;
-  constexpr int N = Vec16<T>::N;
+  const float inv = 1.f / l;  // a window row sees itself: l > 0
+  T* dst = static_cast<T*>(A.o) + ((size_t)tok * A.nkv * A.G + kvh * A.G + r % A.G) * HD + lane * N;
+  T out[N];
 #pragma unroll
-  for (int j = 0; j < 32; j += N) {
-    Vec16<T> v;
-#pragma unroll
-    for (int k = 0; k < N; ++k) v.set(k, acc[j + k] * inv);
-    st16(dst + j, v);
-  }
+  for (int k = 0; k < N; ++k) out[k] = from_f<T>(acc[k] * inv);
+  if constexpr (sizeof(out) == 16)
+    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(out);
+  else if constexpr (sizeof(out) == 8)
+    *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(out);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(out);
 }
 
 template <typename T, int HD>
@@ -271,7 +300,9 @@ cudaError_t launch_simt(const SharedArgs& A, cudaStream_t st) {
 template <typename T, int HD>
 cudaError_t launch_merge(const SharedArgs& A, cudaStream_t st) {
   const int rows = A.B * A.W * A.G;
-  return launch_pdl(shared_merge_kernel<T, HD>, dim3((rows + 31) / 32, A.nkv), dim3(HD), 0, st, A);
+  return launch_pdl(shared_merge_kernel<T, HD>,
+                    dim3((rows + kMergeWarps - 1) / kMergeWarps, A.nkv), dim3(32 * kMergeWarps), 0,
+                    st, A);
 }
 
 }  // namespace

@@ -26,9 +26,10 @@
 //
 // Warps (384 threads): 0-3 softmax of A (thread = row), 4-7 of B, 8 copies Q
 // (TMA) and K/V pages (4 KiB bulk copies in the 8x8-tile operand layout, a lane
-// per page) into a ring, 9 issues the MMAs; 10 and 11 only fill the warpgroup
-// whose registers the softmax warps take over (a row's 128 scores stay in
-// registers): 256 x 208 + 128 x 88 = 384 x 168, what the block was launched with.
+// per page) into a ring, 9 issues the MMAs, 10 plans: it walks the split and
+// publishes the segments ahead of their use.  11 only fills the warpgroup whose
+// registers the softmax warps take over (a row's 128 scores stay in registers):
+// 256 x 208 + 128 x 88 = 384 x 168, what the block was launched with.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -59,36 +60,19 @@ template <int HD> struct Cfg {
   static constexpr uint32_t kSmem = 2 * kQBytes + kRing * kTileBytes + 128;
 };
 
-// what a segment needs beyond its place in the split
-struct Seg : SharedSeg {
-  bool pair;
-  int n, nB;              // tiles of the segment (of stream A in pair mode), of B
-  SeqSpan sp;
-  int n_own, own_keys, pages;
-  int tok0, ntok;         // first query token of the unit, tokens in it
+// A segment as the planner publishes it; n = 0 ends the list.
+struct __align__(16) Seg {
+  int b, kvh, shared;     // sequence (-1: shared unit), kv head, pages it skips
+  int n_own, own_keys;    // cached pages of the range, keys in them (private)
+  int pages;              // pages of the unit: cached, then the window's
+  int t0, t1, n, nB;      // tiles; tiles of stream A, of stream B
+  int pair;
+  int tok0, ntok;         // first query token, tokens
+  int w0;                 // window row of the first token (private)
+  int slot, pad;
 };
+constexpr int kSegs = 4;  // segments published ahead
 
-__device__ __forceinline__ void expand(const SharedArgs& A, int TPB, Seg& g) {
-  const int n = g.t1 - g.t0;
-  if (g.b < 0) {
-    g.tok0 = g.blk * 2 * TPB;
-    g.ntok = min(2 * TPB, A.B * A.W - g.tok0);
-    g.sp = SeqSpan{0, 0};
-    g.n_own = g.own_keys = 0;
-    g.pages = A.nsp;
-  } else {
-    const int w0 = g.blk * 2 * TPB;
-    g.tok0 = g.b * A.W + w0;
-    g.ntok = min(2 * TPB, A.W - w0);
-    g.sp = seq_span(A, g.b, false);
-    g.n_own = own_pages(g.sp);
-    g.own_keys = g.sp.len - g.sp.shared * kPageBlock;
-    g.pages = g.n_own + A.Wp / kPageBlock;
-  }
-  g.pair = g.ntok > TPB;
-  g.n = g.pair ? n : (n + 1) / 2;
-  g.nB = g.pair ? n : n / 2;
-}
 __device__ __forceinline__ int seg_tile(const Seg& g, int x, int j) {
   return g.t0 + (g.pair ? j : 2 * j + x);
 }
@@ -97,20 +81,15 @@ __device__ __forceinline__ int tile_pages(const Seg& g, int t) {
 }
 
 // The order in which K/V tiles are used; the copier and the MMA issuer both
-// follow it.  on_s(x, seg, j) / on_pv(x, seg, j): tile j of stream x; false ends
-// the walk.
-template <typename OnS, typename OnPV>
-__device__ __forceinline__ void run_tiles(const SharedArgs& A, const SharedSplit& S,
-                                          const long long* s_w, int TPB, OnS on_s, OnPV on_pv) {
-  SharedWalk walk;
-  walk.init(S, blockIdx.x);
+// follow it.  get(seg): the next segment; on_s(x, seg, j) / on_pv(x, seg, j):
+// tile j of stream x.  Any of them ends the walk with false.
+template <typename Get, typename OnS, typename OnPV>
+__device__ __forceinline__ void run_tiles(Get get, OnS on_s, OnPV on_pv) {
   Seg cur, nxt;
-  if (!walk.next(A, S, s_w, cur)) return;
-  expand(A, TPB, cur);
+  if (!get(cur)) return;
   if (!on_s(0, cur, 0) || (cur.nB > 0 && !on_s(1, cur, 0))) return;
   while (true) {
-    const bool more = walk.next(A, S, s_w, nxt);
-    if (more) expand(A, TPB, nxt);
+    const bool more = get(nxt);
 #pragma unroll 1
     for (int j = 0; j < cur.n; ++j) {
       const bool last = j + 1 == cur.n;
@@ -201,10 +180,12 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) uint64_t kv_full[kRing], kv_empty[kRing], q_full[2], q_empty[2];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], fin;
+  __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs];
+  __shared__ Seg s_seg[kSegs];
+  __shared__ int s_ids[4][kSharedTilePages];  // page ids of K tiles whose V is still to come
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_any, s_issued, s_taken, s_qissued[2], s_qtaken[2];
+  __shared__ int s_abort, s_issued, s_taken, s_qissued[2], s_qtaken[2];
   __shared__ float2 s_ml[2][128];
-  __shared__ long long s_w[kSharedMaxBatch + 1];
 
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 127) &
                                              ~static_cast<uintptr_t>(127));
@@ -212,10 +193,6 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = A.G;
 
-  pdl_wait();
-  pdl_trigger();
-  const SharedSplit S = shared_split(A, s_w, &s_any);
-  if ((int)blockIdx.x >= S.blocks) return;  // the whole block
   if (threadIdx.x == 32) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&kv_full[i], 1);
@@ -228,6 +205,10 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
       mbar_init(&p_full[x], 4);
       mbar_init(&pv_done[x], 1);
       s_qissued[x] = s_qtaken[x] = 0;
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 10);  // copier, issuer, 8 softmax warps
     }
     mbar_init(&fin, 1);
     s_abort = s_issued = s_taken = 0;
@@ -250,8 +231,71 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
     return false;
   };
 
+  // next published segment, into registers (warp-wide)
+  int seg_i = 0;
+  uint32_t seg_ph = 0;
+  auto get = [&](Seg& g) -> bool {
+    if (!wait(&seg_full[seg_i], seg_ph)) return false;
+    g = s_seg[seg_i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[seg_i]);
+    if (++seg_i == kSegs) {
+      seg_i = 0;
+      seg_ph ^= 1u;
+    }
+    return g.n > 0;
+  };
+
+  pdl_wait();  // nothing of an earlier kernel is read before
+  pdl_trigger();
   if (warp >= 8) {
     regs_down<88>();
+    if (warp == 10) {
+    // ---------------- planner ----------------
+    SharedWalk walk;
+    walk.init(A);
+    SharedSeg u;
+    bool more;
+    do {
+      more = walk.next(A, u);
+      Seg g = {};
+      if (more) {
+        const int n = u.t1 - u.t0;
+        g.b = u.b;
+        g.kvh = u.kvh;
+        g.shared = u.sp.shared;
+        g.t0 = u.t0;
+        g.t1 = u.t1;
+        g.w0 = u.blk * 2 * TPB;
+        if (u.b < 0) {
+          g.tok0 = g.w0;
+          g.ntok = min(2 * TPB, A.B * A.W - g.tok0);
+          g.pages = A.nsp;
+        } else {
+          g.tok0 = u.b * A.W + g.w0;
+          g.ntok = min(2 * TPB, A.W - g.w0);
+          g.n_own = own_pages(u.sp);
+          g.own_keys = u.sp.len - u.sp.shared * kPageBlock;
+          g.pages = g.n_own + A.Wp / kPageBlock;
+        }
+        g.pair = g.ntok > TPB;
+        g.n = g.pair ? n : (n + 1) / 2;
+        g.nB = g.pair ? n : n / 2;
+        g.slot = seg_slot(A, u.unit, blockIdx.x);
+        if (lane == 0) record_unit(A, u);
+      }
+      if (!wait(&seg_empty[seg_i], seg_ph ^ 1u)) break;
+      if (lane == 0) {
+        s_seg[seg_i] = g;
+        mbar_arrive(&seg_full[seg_i]);
+      }
+      __syncwarp();
+      if (++seg_i == kSegs) {
+        seg_i = 0;
+        seg_ph ^= 1u;
+      }
+    } while (more);
+    } else
     if (warp == 8) {
     // ---------------- copier ----------------
     if (lane == 0) tma_prefetch_desc(&mq);
@@ -259,18 +303,35 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
     int st = 0;
     uint32_t ph = 0;
     int issued = 0, flip = 0, nq[2] = {0, 0};
-    // this lane's page of the next K and V tile
-    const bf16* next[2] = {nullptr, nullptr};
-    auto page_of = [&](const Seg& g, int t, int kv) -> const bf16* {
+    // this lane's page id of the next K tile, loaded a tile ahead
+    int next_id = -1, nk = 0, nv = 0;
+    auto id_of = [&](const Seg& g, int t) -> int {
       const int j = t * kSharedTilePages + lane;
-      return lane < kSharedTilePages && t < g.t1 && j < g.pages
-                 ? unit_page<bf16>(A, g, g.sp, g.n_own, j, kv, HD)
-                 : nullptr;
+      return lane < kSharedTilePages && t < g.t1 && j < (g.b < 0 ? g.pages : g.n_own)
+                 ? own_page_id(A, g.b, g.shared, j)
+                 : -1;
     };
     auto load_tile = [&](const Seg& g, int t, int kv) -> bool {
-      const int np = tile_pages(g, t);
-      const bf16* src = next[kv];
-      next[kv] = page_of(g, t + 1, kv);
+      const int np = tile_pages(g, t), j = t * kSharedTilePages + lane;
+      int id = -1;
+      if (kv == 0) {
+        id = next_id;
+        if (lane < kSharedTilePages) s_ids[nk & 3][lane] = id;
+        ++nk;
+        next_id = id_of(g, t + 1);
+      } else {  // V tiles follow in the order of the K tiles, at most 3 behind
+        if (lane < kSharedTilePages) id = s_ids[nv & 3][lane];
+        ++nv;
+      }
+      const bf16* src = nullptr;
+      if (lane < np) {
+        if (g.b >= 0 && j >= g.n_own)
+          src = window_block<bf16>(A, g.b, j - g.n_own, kv, g.kvh, HD);
+        else if (id >= 0 && id < A.num_pages)
+          src = cached_block<bf16>(A, id, kv, g.kvh, HD);
+        else
+          set_err(A.err, WEDLM_DEV_BAD_PAGE);
+      }
       if (!wait(&kv_empty[st], ph ^ 1u)) return false;
       uint8_t* dst = ring + st * C::kTileBytes;
       const unsigned missing = __ballot_sync(0xffffffffu, lane < np && !src);
@@ -307,10 +368,10 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
       return true;
     };
     run_tiles(
-        A, S, s_w, TPB,
+        [&](Seg& g) -> bool { return get(g); },
         [&](int x, const Seg& g, int j) -> bool {
           if (j == 0) {
-            if (x == 0) next[0] = page_of(g, g.t0, 0);
+            if (x == 0) next_id = id_of(g, g.t0);
             if (g.pair) {
               if (!load_q(g, x, g.tok0 + x * TPB)) return false;
             } else if (x == 0) {
@@ -321,7 +382,6 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
           return (g.pair && x == 1) || load_tile(g, seg_tile(g, x, j), 0);
         },
         [&](int x, const Seg& g, int j) -> bool {
-          if (j == 0 && x == 0) next[1] = page_of(g, g.t0, 1);
           return (g.pair && x == 1) || load_tile(g, seg_tile(g, x, j), 1);
         });
     } else if (warp == 9) {
@@ -351,7 +411,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
       return true;
     };
     run_tiles(
-        A, S, s_w, TPB,
+        [&](Seg& g) -> bool { return get(g); },
         [&](int x, const Seg& g, int j) -> bool {
           if (j == 0) {
             if (g.pair) {
@@ -439,15 +499,12 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
     const float sc = A.scale_log2;
     uint32_t sph = 0, dph = 0;  // phases of s_full and of pv_done
     auto both = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
-    SharedWalk walk;
-    walk.init(S, blockIdx.x);
     Seg g;
-    while (walk.next(A, S, s_w, g)) {
-      expand(A, TPB, g);
+    while (get(g)) {
       const int nx = x ? g.nB : g.n;
       // token of this row within the unit, its window row
       const int utok = (g.pair ? x * TPB : 0) + r / G;
-      const int p_row = g.b < 0 ? 0 : g.blk * 2 * TPB + utok;
+      const int p_row = g.w0 + utok;
       const bool valid = r < TPB * G && utok < g.ntok;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nx; ++j) {
@@ -521,10 +578,8 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
       if (nx > 0) wait(&pv_done[x], dph ^ 1u);
       tc_fence_after();
       const int urows = g.b < 0 ? A.srows : A.prows;
-      const size_t slot = seg_slot(A, g.unit, blockIdx.x);
-      float4* po = (g.b < 0 ? A.part_s : A.part_p) + slot * (HD / 4) * urows;
-      float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + slot * urows;
-      if (threadIdx.x == 0) record_unit(A, g);
+      float* po = (g.b < 0 ? A.part_s : A.part_p) + (size_t)g.slot * urows * HD;
+      float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + (size_t)g.slot * urows;
       if (g.pair) {
         const int row = x * TPB * G + r;
 #pragma unroll
@@ -533,9 +588,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
           ld32(tO + c, o);
           if (valid)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              po[(size_t)(c / 4 + k) * urows + row] =
-                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            for (int k = 0; k < 32; k += 8) st_sector(po + (size_t)row * HD + c + k, o + k);
         }
         if (valid) ml[row] = make_float2(m, l);
         tc_fence_before();
@@ -565,9 +618,8 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
           }
           if (valid)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              po[(size_t)((x * HD / 2 + c) / 4 + k) * urows + r] =
-                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            for (int k = 0; k < 32; k += 8)
+              st_sector(po + (size_t)r * HD + x * (HD / 2) + c + k, o + k);
         }
         if (valid && x == 0) ml[r] = make_float2(M, l * am + o_ml.y * ao);
         tc_fence_before();

@@ -40,7 +40,7 @@ struct SharedArgs {
   int ucost, shared_cost, private_cost, min_share;
   int grid;
   // workspace
-  float4 *part_s, *part_p;        // [slot][hd/4][rows of a unit] partial O
+  float *part_s, *part_p;         // [slot][rows of a unit][hd] partial O
   float2 *ml_s, *ml_p;            // [slot][rows of a unit] running max (log2 units), row sum
   int2* unit_blocks;              // [unit] blocks of the first and last tile
 };
@@ -66,107 +66,114 @@ __device__ __forceinline__ int own_tiles(const SharedArgs& A, const SeqSpan& s) 
   return (own_pages(s) + A.Wp / kPageBlock + kSharedTilePages - 1) / kSharedTilePages;
 }
 
-// The split, built once per block by all of its threads.  s_w: B + 1 words of
-// shared memory, the weighted start of each sequence's private units.
-struct SharedSplit {
-  long long shared_unit;  // weight of one shared unit (0: nobody shares)
-  long long shared_total, total;
-  int shared_tiles, blocks;
+// One segment: tiles t0 .. t1-1 of a unit of T tiles.
+struct SharedSeg {
+  int unit;             // index over all units (shared ones first)
+  int b;                // sequence of a private unit, -1: shared
+  int kvh, blk;         // kv head, row block
+  int t0, t1, T;
+  SeqSpan sp;           // of sequence b
 };
-__device__ inline SharedSplit shared_split(const SharedArgs& A, long long* s_w, int* s_any) {
-  if (threadIdx.x == 0) *s_any = 0;
-  __syncthreads();
-  for (int b = threadIdx.x; b < A.B; b += blockDim.x) {
-    const SeqSpan sp = seq_span(A, b, blockIdx.x == 0);
-    if (sp.shared) *s_any = 1;
-    s_w[b] = (long long)A.nkv * A.pblocks *
-             (A.ucost + (long long)own_tiles(A, sp) * A.private_cost);
+
+// Walks the segments of this block in tile order; one warp runs it, all lanes
+// alike.  Tile t of a unit starts ucost + t * cost after the unit, and a block
+// owns the tiles that start in its share of the total weight.
+struct SharedWalk {
+  long long u0, w0, w1;  // weighted start of the next unit, the block's share
+  long long shared_unit, shared_total;
+  int shared_tiles, u, b, k;  // next unit: shared unit u, or unit k of sequence b
+
+  __device__ long long seq_weight(const SharedArgs& A, const SeqSpan& sp) const {
+    return (long long)A.nkv * A.pblocks *
+           (A.ucost + (long long)own_tiles(A, sp) * A.private_cost);
   }
-  __syncthreads();
-  if (threadIdx.x < 32) {  // exclusive prefix sums, in place
-    const int lane = threadIdx.x, per = (A.B + 31) / 32;
-    const int b0 = min(A.B, lane * per), b1 = min(A.B, b0 + per);
+  __device__ void init(const SharedArgs& A) {
+    const int lane = threadIdx.x & 31;
+    const int per = (A.B + 31) / 32, b0 = min(A.B, lane * per), b1 = min(A.B, b0 + per);
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += s_w[b];
+    bool any = false;
+    for (int i = b0; i < b1; ++i) {
+      const SeqSpan sp = seq_span(A, i, blockIdx.x == 0);
+      any |= sp.shared > 0;
+      sum += seq_weight(A, sp);
+    }
+    any = __any_sync(0xffffffffu, any);
     long long incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    long long acc = incl - sum;
-    for (int b = b0; b < b1; ++b) {
-      const long long x = s_w[b];
-      s_w[b] = acc;
-      acc += x;
+    // nothing to do for the shared pages when no sequence takes part
+    shared_tiles = any ? (A.nsp + kSharedTilePages - 1) / kSharedTilePages : 0;
+    shared_unit = any ? A.ucost + (long long)shared_tiles * A.shared_cost : 0;
+    shared_total = shared_unit * A.nkv * A.sblocks;
+    const long long total = shared_total + __shfl_sync(0xffffffffu, incl, 31);
+    // a share is never shorter than min_share >= a tile, so that it holds a
+    // tile's start wherever it lies inside a unit
+    const int blocks = (int)max(1LL, min((long long)A.grid, total / A.min_share));
+    u = b = k = 0;
+    w0 = w1 = u0 = 0;
+    if ((int)blockIdx.x >= blocks) {
+      b = A.B;
+      return;
     }
-    if (lane == 31) s_w[A.B] = incl;
+    w0 = blockIdx.x * total / blocks;
+    w1 = (blockIdx.x + 1) * total / blocks;
+    if (w0 < shared_total) {
+      u = (int)(w0 / shared_unit);
+      u0 = u * shared_unit;
+    } else {
+      u = A.nkv * A.sblocks;
+      const long long r = w0 - shared_total;
+      const int owner = __ffs(__ballot_sync(0xffffffffu, incl > r)) - 1;
+      long long at = incl - sum;
+      int i = b0;
+      if (lane == owner)
+        for (;; ++i) {
+          const long long w = seq_weight(A, seq_span(A, i, false));
+          if (r < at + w) break;
+          at += w;
+        }
+      b = __shfl_sync(0xffffffffu, i, owner);
+      at = __shfl_sync(0xffffffffu, at, owner);
+      const SeqSpan sp = seq_span(A, b, false);
+      const long long uw = seq_weight(A, sp) / (A.nkv * A.pblocks);
+      k = (int)((r - at) / uw);
+      u0 = shared_total + at + k * uw;
+    }
   }
-  __syncthreads();
-  SharedSplit S;
-  S.shared_tiles = *s_any ? (A.nsp + kSharedTilePages - 1) / kSharedTilePages : 0;
-  S.shared_unit = S.shared_tiles ? A.ucost + (long long)S.shared_tiles * A.shared_cost : 0;
-  S.shared_total = S.shared_unit * A.nkv * A.sblocks;
-  S.total = S.shared_total + s_w[A.B];
-  // a share holds at least one tile start wherever it lies inside a unit
-  S.blocks = (int)max(1LL, min((long long)A.grid, S.total / A.min_share));
-  return S;
-}
-
-// One segment: tiles t0 .. t1-1 of a unit.
-struct SharedSeg {
-  int unit;       // index over all units (shared ones first)
-  int b;          // sequence of a private unit, -1: shared
-  int kvh, blk;   // kv head, row block
-  int t0, t1, T;  // tiles of the segment, of the unit
-};
-
-// Walks the segments of one block in tile order.
-struct SharedWalk {
-  long long w, w1;  // weighted position, end of the share
-  __device__ void init(const SharedSplit& S, int block) {
-    w = block * S.total / S.blocks;
-    w1 = (block + 1) * S.total / S.blocks;
-  }
-  // tile t of a unit starts ucost + t * cost after the unit; a block owns the
-  // tiles that start in its share
-  __device__ bool next(const SharedArgs& A, const SharedSplit& S, const long long* s_w,
-                       SharedSeg& g) {
-    while (w < w1) {
-      long long u0, uw;
+  __device__ bool next(const SharedArgs& A, SharedSeg& g) {
+    while (b < A.B && u0 < w1) {
       int cost;
-      if (w < S.shared_total) {
-        const int u = (int)(w / S.shared_unit);
-        u0 = u * S.shared_unit;
-        uw = S.shared_unit;
+      if (u < A.nkv * A.sblocks && shared_tiles) {
         g.unit = u;
         g.b = -1;
         g.kvh = u / A.sblocks;
-        g.blk = u % A.sblocks;
-        g.T = S.shared_tiles;
+        g.blk = u - g.kvh * A.sblocks;
+        g.T = shared_tiles;
+        g.sp = SeqSpan{0, 0};
         cost = A.shared_cost;
+        ++u;
       } else {
-        const long long r = w - S.shared_total;
-        int lo = 0, hi = A.B - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (s_w[mid] <= r) lo = mid; else hi = mid - 1;
-        }
         const int per = A.nkv * A.pblocks;
-        uw = (s_w[lo + 1] - s_w[lo]) / per;
-        const int k = (int)((r - s_w[lo]) / uw);
-        u0 = S.shared_total + s_w[lo] + k * uw;
-        g.unit = A.nkv * A.sblocks + lo * per + k;
-        g.b = lo;
+        g.unit = A.nkv * A.sblocks + b * per + k;
+        g.b = b;
         g.kvh = k / A.pblocks;
-        g.blk = k % A.pblocks;
+        g.blk = k - g.kvh * A.pblocks;
+        g.sp = seq_span(A, b, false);
+        g.T = own_tiles(A, g.sp);
         cost = A.private_cost;
-        g.T = (int)((uw - A.ucost) / cost);
+        if (++k == per) {
+          k = 0;
+          ++b;
+        }
       }
-      const long long first = w - u0 - A.ucost, end = w1 - u0 - A.ucost;
-      g.t0 = first <= 0 ? 0 : (int)((first + cost - 1) / cost);
-      g.t1 = end <= 0 ? 0 : (int)min((long long)g.T, (end + cost - 1) / cost);
-      w = u0 + uw;
+      const long long first = w0 - u0 - A.ucost, end = w1 - u0 - A.ucost;
+      const long long len = (long long)g.T * cost;
+      g.t0 = first <= 0 ? 0 : first >= len ? g.T : (int)((first + cost - 1) / cost);
+      g.t1 = end <= 0 ? 0 : end >= len ? g.T : (int)((end + cost - 1) / cost);
+      u0 += A.ucost + len;
       if (g.t0 < g.t1) return true;
     }
     return false;
@@ -179,29 +186,34 @@ __device__ __forceinline__ int seg_slot(const SharedArgs& A, int unit, int block
   return (unit < ns ? unit : unit - ns) + block;
 }
 
+// 8 floats to one 32-byte sector
+__device__ __forceinline__ void st_sector(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // one thread of the block records the unit's first and last block
 __device__ __forceinline__ void record_unit(const SharedArgs& A, const SharedSeg& g) {
   if (g.t0 == 0) A.unit_blocks[g.unit].x = blockIdx.x;
   if (g.t1 == g.T) A.unit_blocks[g.unit].y = blockIdx.x;
 }
 
-// Page `j` of a unit (its keys 16j .. 16j+15): cached pages first, then the
-// window block's.  Sets the 16-token K (kv = 0) or V block of kv head kvh, or
-// null for a page id out of range (recorded in the error word).
+// Page `j` of a unit (its keys 16j .. 16j+15): n_own cached pages, then the
+// window block's.  own_page_id: the id of a cached one, as the table has it.
+__device__ __forceinline__ int own_page_id(const SharedArgs& A, int b, int shared, int j) {
+  return b < 0 ? __ldg(A.shared + j) : __ldg(A.page_table + (size_t)b * A.max_pages + shared + j);
+}
 template <typename T>
-__device__ __forceinline__ const T* unit_page(const SharedArgs& A, const SharedSeg& g,
-                                              const SeqSpan& sp, int n_own, int j, int kv, int hd) {
-  const size_t blockn = (size_t)kPageBlock * hd;
-  if (g.b >= 0 && j >= n_own)
-    return static_cast<const T*>(A.kv_win) +
-           (((size_t)g.b * 2 + kv) * A.nkv + g.kvh) * A.Wp * hd + (size_t)(j - n_own) * blockn;
-  const int id = g.b < 0 ? A.shared[j]
-                         : A.page_table[(size_t)g.b * A.max_pages + sp.shared + j];
-  if (id < 0 || id >= A.num_pages) {
-    set_err(A.err, WEDLM_DEV_BAD_PAGE);
-    return nullptr;
-  }
-  return static_cast<const T*>(A.pool) + (((size_t)id * 2 + kv) * A.nkv + g.kvh) * blockn;
+__device__ __forceinline__ const T* cached_block(const SharedArgs& A, int id, int kv, int kvh,
+                                                 int hd) {
+  return static_cast<const T*>(A.pool) + (((size_t)id * 2 + kv) * A.nkv + kvh) * kPageBlock * hd;
+}
+template <typename T>
+__device__ __forceinline__ const T* window_block(const SharedArgs& A, int b, int j, int kv, int kvh,
+                                                 int hd) {
+  return static_cast<const T*>(A.kv_win) +
+         ((((size_t)b * 2 + kv) * A.nkv + kvh) * A.Wp + j * kPageBlock) * hd;
 }
 
 // fp32: urows query rows per unit, whatever tokens they belong to
