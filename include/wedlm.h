@@ -475,6 +475,9 @@ size_t wedlm_shared_attention_workspace(const wedlm_shared_attn_args *args);
  *    need one each.  No context and no allocation.  The result is the same,
  *    bit for bit, whenever the inputs are.
  *  - q, kv_pool, kv_win and o are 16-byte aligned and contiguous.
+ *  - Limit: n_kv_heads * (row blocks of the batch * S/8 + B * row blocks of a
+ *    window * max_pages_per_seq/8) stays below 2^31 (a row block: 128 rows or
+ *    more in bf16, 64 in fp32, of the G rows per token).
  * Returns WEDLM_ERR_INVALID_ARG (nothing enqueued), WEDLM_ERR_CAPACITY for a
  * workspace that is too small, or WEDLM_ERR_CUDA. */
 int wedlm_shared_attention(const wedlm_shared_attn_args *args, void *stream);

@@ -52,6 +52,16 @@ bool shared_plan(const wedlm_shared_attn_args& a, SharedPlan* P) {
     A.ucost = 1;
     A.shared_cost = A.private_cost = A.min_share = 1;
   }
+  // the split counts in 31 bits: where full tables could pass that, a tile and a
+  // unit's ends weigh 1, and beyond that the call is refused
+  auto weight = [&]() {
+    const long long st = (A.nsp + kSharedTilePages - 1) / kSharedTilePages;
+    const long long pt = (A.max_pages + A.Wp / kPageBlock + kSharedTilePages - 1) / kSharedTilePages;
+    return (long long)A.nkv * (A.sblocks * (A.ucost + st * A.shared_cost) +
+                               (long long)A.B * A.pblocks * (A.ucost + pt * A.private_cost));
+  };
+  if (weight() > INT32_MAX) A.ucost = A.shared_cost = A.private_cost = A.min_share = 1;
+  if (weight() > INT32_MAX) return false;
   const long long su = (long long)A.nkv * A.sblocks, pu = (long long)A.B * A.nkv * A.pblocks;
   if (su + pu > (1 << 24)) return false;
   const size_t ss = (size_t)su + kSharedMaxGrid, ps = (size_t)pu + kSharedMaxGrid;

@@ -224,9 +224,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(SharedAr
   const int us = kvh * A.sblocks + r / A.srows, is = r % A.srows;
   const int up = A.nkv * A.sblocks + (b * A.nkv + kvh) * A.pblocks + pr / A.prows;
   const int ip = pr % A.prows;
-  const int2 bs = A.unit_blocks[us], bp = A.unit_blocks[up];
-  const int ns = seq_span(A, b, false).shared ? bs.y - bs.x + 1 : 0;
-  const int n = ns + bp.y - bp.x + 1;
+  // clamped: after a wait that expired the records may be missing
+  int2 bs = A.unit_blocks[us], bp = A.unit_blocks[up];
+  bs.x = max(0, min(bs.x, A.grid - 1));
+  bp.x = max(0, min(bp.x, A.grid - 1));
+  const int ns = seq_span(A, b, false).shared ? max(0, min(bs.y, A.grid - 1) - bs.x + 1) : 0;
+  const int n = ns + max(0, min(bp.y, A.grid - 1) - bp.x + 1);
   float M = -INFINITY, l = 0.f, acc[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) acc[k] = 0.f;

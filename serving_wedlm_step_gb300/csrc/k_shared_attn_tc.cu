@@ -24,12 +24,18 @@
 // tensor core runs them in that order, so S may follow P V into the columns that
 // P V reads.
 //
+// Code size: a unit's first and last tiles, its end and the single-thread roles
+// run code that the other warps' loops push out of the instruction caches, and
+// every line fetched again costs them hundreds of cycles (masking 128 unrolled
+// columns took 25,000 cycles).  Everything but the softmax of a full tile is
+// kept in rolled loops.
+//
 // Warps (384 threads): 0-3 softmax of A (thread = row), 4-7 of B, 8 copies Q
 // (TMA) and K/V pages (4 KiB bulk copies in the 8x8-tile operand layout, a lane
 // per page) into a ring, 9 issues the MMAs, 10 plans: it walks the split and
-// publishes the segments ahead of their use.  11 only fills the warpgroup whose
-// registers the softmax warps take over (a row's 128 scores stay in registers):
-// 256 x 208 + 128 x 88 = 384 x 168, what the block was launched with.
+// publishes the segments ahead of their use; 11 is idle.  A row's 128 scores are
+// taken in two halves of 64, the second one read from TMEM twice, so that the
+// softmax fits the 168 registers a thread has.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -45,13 +51,6 @@ constexpr int kThreads = 384;
 constexpr int kRing = 4;                 // K/V tiles in shared memory
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 constexpr float kRaise = 8.f;            // log2 units
-
-template <int N> __device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N> __device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 template <int HD> struct Cfg {
   static constexpr uint32_t kPage = kPageBlock * HD * 2;
@@ -156,6 +155,15 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void ld16(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : R8(v, 0), R8(v, 8)
+      : "r"(taddr)
+      : "memory");
+}
 #undef R8
 #define W8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), \
                  "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
@@ -168,7 +176,63 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
       W8(r, 0), W8(r, 8), W8(r, 16), W8(r, 24)
       : "memory");
 }
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      W8(r, 0), W8(r, 8)
+      : "memory");
+}
 #undef W8
+// two 32-bit lanes at once
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max64(const float* v) {
+  float mx[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    mx[k] = fmaxf(v[k], v[k + 4]);
+#pragma unroll
+    for (int c = 8; c < 64; c += 8) mx[k] = fmaxf(mx[k], fmaxf(v[c + k], v[c + k + 4]));
+  }
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+// p = 2^(v * sc + nm) of 64 columns to 32 columns of bf16 pairs; their sum
+__device__ __forceinline__ float exp64(uint32_t taddr, const float* v, float sc, float nm) {
+  const uint64_t sc2 = pack2(sc, sc), nm2 = pack2(nm, nm);
+  uint64_t ps[2] = {0, 0};
+  uint32_t pk[32];
+#pragma unroll
+  for (int c = 0; c < 64; c += 2) {
+    float p0, p1;
+    unpack2(fma2(pack2(v[c], v[c + 1]), sc2, nm2), p0, p1);
+    p0 = ex2_approx(p0);
+    p1 = ex2_approx(p1);
+    ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], pack2(p0, p1));
+    const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+    pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
+  }
+  st32(taddr, pk);
+  float s0, s1;
+  unpack2(add2(ps[0], ps[1]), s0, s1);
+  return s0 + s1;
+}
 __device__ __forceinline__ void wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -180,7 +244,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) uint64_t kv_full[kRing], kv_empty[kRing], q_full[2], q_empty[2];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], fin;
-  __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs];
+  __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], joined;
   __shared__ Seg s_seg[kSegs];
   __shared__ int s_ids[4][kSharedTilePages];  // page ids of K tiles whose V is still to come
   __shared__ uint32_t s_tmem;
@@ -210,6 +274,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_empty[i], 10);  // copier, issuer, 8 softmax warps
     }
+    mbar_init(&joined, 8);
     mbar_init(&fin, 1);
     s_abort = s_issued = s_taken = 0;
     mbar_fence_init();
@@ -223,12 +288,14 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort = &s_abort;
+  // warp-wide and bounded: what follows is executed by the whole warp together
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (mbar_wait(bar, parity, A.err)) return true;
-    *abort = 1;
-    return false;
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok && !*abort) {
+      ok = mbar_wait(bar, parity, A.err);
+      if (!ok) *abort = 1;
+    }
+    return __all_sync(0xffffffffu, ok);
   };
 
   // next published segment, into registers (warp-wide)
@@ -249,7 +316,6 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
   pdl_wait();  // nothing of an earlier kernel is read before
   pdl_trigger();
   if (warp >= 8) {
-    regs_down<88>();
     if (warp == 10) {
     // ---------------- planner ----------------
     SharedWalk walk;
@@ -257,7 +323,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
     SharedSeg u;
     bool more;
     do {
-      more = walk.next(A, u);
+      more = __shfl_sync(0xffffffffu, walk.next(A, u), 0);
       Seg g = {};
       if (more) {
         const int n = u.t1 - u.t0;
@@ -431,7 +497,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
             const uint32_t id =
                 idesc_bf16_m128(tile_pages(g, seg_tile(g, x, j)) * kPageBlock);
             const uint32_t d = tmem + kColS + (uint32_t)(x * 128);
-#pragma unroll
+#pragma unroll 1  // rolled: see the note on code size
             for (int k = 0; k < HD / 16; ++k)  // 16 dims: two 8-dim groups
               tc_mma_f16(d, dq + k * 256, dk + k * 16, id, k ? 1u : 0u);
             tc_commit(&s_full[x]);
@@ -473,9 +539,9 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
             const uint64_t dv = dv0 + (uint64_t)(vst * C::kTileBytes >> 4);
             const uint32_t d = tmem + kColO + (uint32_t)(x * 128);
             const uint32_t p = tmem + kColS + (uint32_t)(x * 128);
-#pragma unroll
-            for (int k = 0; k < kSharedTilePages; ++k)  // 16 keys: 8 columns of P
-              if (k < np) mma_ts(d, p + k * 8, dv + k * (HD * 2), idPV, (j || k) ? 1u : 0u);
+#pragma unroll 1
+            for (int k = 0; k < np; ++k)  // 16 keys: 8 columns of P
+              mma_ts(d, p + k * 8, dv + k * (HD * 2), idPV, (j || k) ? 1u : 0u);
             tc_commit(&pv_done[x]);
             if (!g.pair || x == 1) tc_commit(&kv_empty[vst]);
           }
@@ -490,7 +556,6 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
     }
   } else {
     // ---------------- softmax ----------------
-    regs_up<208>();
     const int x = warp >> 2;                       // stream
     const int r = threadIdx.x & 127;               // row of the stream's row block
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
@@ -498,7 +563,15 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
     const uint32_t tO = tmem + lane_off + kColO + (uint32_t)(x * 128);
     const float sc = A.scale_log2;
     uint32_t sph = 0, dph = 0;  // phases of s_full and of pv_done
-    auto both = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    // both streams' warps meet; an mbarrier and not a named one, so that a wait
+    // that expired elsewhere cannot leave one side here for good
+    uint32_t jph = 0;
+    auto both = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&joined);
+      wait(&joined, jph);
+      jph ^= 1u;
+    };
     Seg g;
     while (get(g)) {
       const int nx = x ? g.nB : g.n;
@@ -512,62 +585,55 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
         wait(&s_full[x], sph);
         sph ^= 1u;
         tc_fence_after();
-        float v[128];
-        ld64(tS, v);
-        ld64(tS + 64, v + 64);
-        // a tile of visible keys needs no mask
+        // what this row does not see becomes -inf, in TMEM and in a rolled loop:
+        // only a unit's last tiles need it
         if (np < kSharedTilePages || (g.b >= 0 && (t + 1) * kSharedTile > g.own_keys)) {
           const int c_own = g.b < 0 ? np * kPageBlock : g.own_keys - t * kSharedTile;
           const int c_win = g.n_own * kPageBlock - t * kSharedTile;
           const int c_end = g.b < 0 ? 0 : c_win + p_row + 1;  // window keys up to this row
+#pragma unroll 1
+          for (int c0 = 0; c0 < kSharedTile; c0 += 16) {
+            if (c0 + 16 <= c_own) continue;  // the same for the warpgroup
+            float e[16];
+            uint32_t u[16];
+            ld16(tS + c0, e);
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!(c < c_own || (c >= c_win && c < c_end && c < np * kPageBlock))) v[c] = -INFINITY;
+            for (int i = 0; i < 16; ++i) {
+              const int c = c0 + i;
+              u[i] = c < c_own || (c >= c_win && c < c_end) ? __float_as_uint(e[i]) : 0xff800000u;
+            }
+            st16(tS + c0, u);
+          }
+          wait_st();
         }
-        float mx[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mx[k] = fmaxf(v[k], v[k + 4]);
-#pragma unroll
-          for (int c = 8; c < 128; c += 8)
-            mx[k] = fmaxf(mx[k], fmaxf(v[c + k], v[c + k + 4]));
-        }
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        float v[64];
+        ld64(tS + 64, v);
+        const float mx1 = max64(v);
+        ld64(tS, v);
+        const float mt = fmaxf(mx1, max64(v)) * sc;
         const bool raise = mt > m + kRaise;
         if (__any_sync(0xffffffffu, raise)) {  // TMEM accesses are warp-wide
           if (j > 0) {
             const float a = !raise ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - mt);
             wait(&pv_done[x], dph ^ 1u);  // P V of the tile before is in O
             tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 16) {
+              float o[16];
+              uint32_t u[16];
+              ld16(tO + c, o);
 #pragma unroll
-            for (int c = 0; c < HD; c += 32) {
-              float o[32];
-              uint32_t u[32];
-              ld32(tO + c, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * a);
-              st32(tO + c, u);
+              for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * a);
+              st16(tO + c, u);
             }
             l *= a;
           }
           if (raise) m = mt;
         }
         const float nm = m == -INFINITY ? 0.f : -m;
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pk[32];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float p0 = ex2_approx(fmaf(v[64 * h + c], sc, nm));
-            const float p1 = ex2_approx(fmaf(v[64 * h + c + 1], sc, nm));
-            ps[(c >> 1) & 3] += p0 + p1;
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-            pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
-          }
-          st32(tS + 32 * h, pk);
-        }
-        l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        l += exp64(tS, v, sc, nm);  // P over the columns just read
+        ld64(tS + 64, v);
+        l += exp64(tS + 32, v, sc, nm);
         wait_st();
         tc_fence_before();
         __syncwarp();
@@ -582,7 +648,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
       float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + (size_t)g.slot * urows;
       if (g.pair) {
         const int row = x * TPB * G + r;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           float o[32];
           ld32(tO + c, o);
@@ -604,7 +670,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
         const float ao = o_ml.x == -INFINITY ? 0.f : ex2_approx(o_ml.x - M);
         const float fa = x ? ao : am, fb = x ? am : ao;  // factors of A's and B's O
         const uint32_t t0 = tmem + lane_off + kColO + (uint32_t)(x * HD / 2);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < HD / 2; c += 32) {
           float o[32];
           ld32(t0 + c, o);

@@ -77,69 +77,71 @@ struct SharedSeg {
 
 // Walks the segments of this block in tile order; one warp runs it, all lanes
 // alike.  Tile t of a unit starts ucost + t * cost after the unit, and a block
-// owns the tiles that start in its share of the total weight.
+// owns the tiles that start in its share of the total weight.  The host keeps
+// the total below 2^31, so that the divisions are 32 bits wide: the planner runs
+// before the first copy can start.
 struct SharedWalk {
-  long long u0, w0, w1;  // weighted start of the next unit, the block's share
-  long long shared_unit, shared_total;
+  int u0, w0, w1;       // weighted start of the next unit, the block's share
   int shared_tiles, u, b, k;  // next unit: shared unit u, or unit k of sequence b
 
-  __device__ long long seq_weight(const SharedArgs& A, const SeqSpan& sp) const {
-    return (long long)A.nkv * A.pblocks *
-           (A.ucost + (long long)own_tiles(A, sp) * A.private_cost);
+  __device__ int unit_weight(const SharedArgs& A, const SeqSpan& sp) const {
+    return A.ucost + own_tiles(A, sp) * A.private_cost;
   }
   __device__ void init(const SharedArgs& A) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, units = A.nkv * A.pblocks;
     const int per = (A.B + 31) / 32, b0 = min(A.B, lane * per), b1 = min(A.B, b0 + per);
-    long long sum = 0;
+    int sum = 0;
     bool any = false;
+#pragma unroll 1
     for (int i = b0; i < b1; ++i) {
       const SeqSpan sp = seq_span(A, i, blockIdx.x == 0);
       any |= sp.shared > 0;
-      sum += seq_weight(A, sp);
+      sum += units * unit_weight(A, sp);
     }
     any = __any_sync(0xffffffffu, any);
-    long long incl = sum;
+    int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
     // nothing to do for the shared pages when no sequence takes part
     shared_tiles = any ? (A.nsp + kSharedTilePages - 1) / kSharedTilePages : 0;
-    shared_unit = any ? A.ucost + (long long)shared_tiles * A.shared_cost : 0;
-    shared_total = shared_unit * A.nkv * A.sblocks;
-    const long long total = shared_total + __shfl_sync(0xffffffffu, incl, 31);
+    const int shared_unit = any ? A.ucost + shared_tiles * A.shared_cost : 0;
+    const int shared_total = shared_unit * A.nkv * A.sblocks;
+    const unsigned total = shared_total + __shfl_sync(0xffffffffu, incl, 31);
     // a share is never shorter than min_share >= a tile, so that it holds a
     // tile's start wherever it lies inside a unit
-    const int blocks = (int)max(1LL, min((long long)A.grid, total / A.min_share));
+    const unsigned blocks = max(1u, min((unsigned)A.grid, total / (unsigned)A.min_share));
     u = b = k = 0;
     w0 = w1 = u0 = 0;
-    if ((int)blockIdx.x >= blocks) {
+    if (blockIdx.x >= blocks) {
       b = A.B;
       return;
     }
-    w0 = blockIdx.x * total / blocks;
-    w1 = (blockIdx.x + 1) * total / blocks;
+    const unsigned share = total / blocks, extra = total - share * blocks;
+    w0 = blockIdx.x * share + min(blockIdx.x, extra);
+    w1 = w0 + share + (blockIdx.x < extra ? 1 : 0);
     if (w0 < shared_total) {
-      u = (int)(w0 / shared_unit);
+      u = (unsigned)w0 / (unsigned)shared_unit;
       u0 = u * shared_unit;
     } else {
       u = A.nkv * A.sblocks;
-      const long long r = w0 - shared_total;
+      const int r = w0 - shared_total;
       const int owner = __ffs(__ballot_sync(0xffffffffu, incl > r)) - 1;
-      long long at = incl - sum;
-      int i = b0;
-      if (lane == owner)
-        for (;; ++i) {
-          const long long w = seq_weight(A, seq_span(A, i, false));
+      int at = incl - sum, i = b0;
+      if (lane == owner) {
+#pragma unroll 1
+        for (; i + 1 < b1; ++i) {
+          const int w = units * unit_weight(A, seq_span(A, i, false));
           if (r < at + w) break;
           at += w;
         }
+      }
       b = __shfl_sync(0xffffffffu, i, owner);
       at = __shfl_sync(0xffffffffu, at, owner);
-      const SeqSpan sp = seq_span(A, b, false);
-      const long long uw = seq_weight(A, sp) / (A.nkv * A.pblocks);
-      k = (int)((r - at) / uw);
+      const int uw = unit_weight(A, seq_span(A, b, false));
+      k = (unsigned)(r - at) / (unsigned)uw;
       u0 = shared_total + at + k * uw;
     }
   }
@@ -169,10 +171,9 @@ struct SharedWalk {
           ++b;
         }
       }
-      const long long first = w0 - u0 - A.ucost, end = w1 - u0 - A.ucost;
-      const long long len = (long long)g.T * cost;
-      g.t0 = first <= 0 ? 0 : first >= len ? g.T : (int)((first + cost - 1) / cost);
-      g.t1 = end <= 0 ? 0 : end >= len ? g.T : (int)((end + cost - 1) / cost);
+      const int first = w0 - u0 - A.ucost, end = w1 - u0 - A.ucost, len = g.T * cost;
+      g.t0 = first <= 0 ? 0 : first >= len ? g.T : (first + cost - 1) / cost;
+      g.t1 = end <= 0 ? 0 : end >= len ? g.T : (end + cost - 1) / cost;
       u0 += A.ucost + len;
       if (g.t0 < g.t1) return true;
     }
