@@ -114,8 +114,8 @@ extern "C" int wedlm_shared_attention(const wedlm_shared_attn_args* a, void* str
   A.o = a->o;
   A.err = a->error;
   char* ws = static_cast<char*>(a->workspace);
-  A.part_s = reinterpret_cast<float*>(ws);
-  A.part_p = reinterpret_cast<float*>(ws + P.off_part_p);
+  A.part_s = reinterpret_cast<float4*>(ws);
+  A.part_p = reinterpret_cast<float4*>(ws + P.off_part_p);
   A.ml_s = reinterpret_cast<float2*>(ws + P.off_ml_s);
   A.ml_p = reinterpret_cast<float2*>(ws + P.off_ml_p);
   A.unit_blocks = reinterpret_cast<int2*>(ws + P.off_units);

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
     }
     if (tid == 0) record_unit(A, g);
     const size_t slot = seg_slot(A, g.unit, blockIdx.x);
-    float* po = (g.b < 0 ? A.part_s : A.part_p) + slot * urows * HD;
+    float4* po = (g.b < 0 ? A.part_s : A.part_p) + slot * urows * (HD / 4);
     float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + slot * urows;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
       if (r >= nrows) continue;
 #pragma unroll
       for (int j = 0; j < ND; ++j)
-        *reinterpret_cast<float4*>(po + (size_t)r * HD + tx * 4 + 64 * j) =
+        po[(size_t)(tx + 16 * j) * urows + r] =
             make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
       if (tx == 0) ml[r] = make_float2(m[i], l[i]);
     }
@@ -207,21 +207,24 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
 }
 
 // The merge: row r of kv head kvh joins the partials of its shared unit (when
-// its sequence takes part) and of its private unit, in slot order.  A warp per
-// row, HD/32 dims a lane: first the weights, 2^(m_i - M) / sum, of up to 32
-// partials at a time (a lane each), then their O, eight loads in flight.
-constexpr int kMergeWarps = 4;
-template <typename T, int HD>
-__global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(SharedArgs A) {
-  constexpr int N = HD / 32;
+// its sequence takes part) and of its private unit, in slot order.  A block takes
+// RPB rows; a warp 16 dims of them: 32 / RPB groups of lanes share a row's
+// partials out among them, so that few rows with many partials do not wait for
+// them one by one.  Partials lie dims-major, so that both the writer's warps (a
+// lane per row) and these loads touch runs of rows.
+template <typename T, int HD, int RPB>
+__global__ void __launch_bounds__(2 * HD) shared_merge_kernel(const __grid_constant__ SharedArgs A) {
+  constexpr int NG = 32 / RPB;       // lane groups of a row
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, d40 = threadIdx.x / 32 * 4;
   const int kvh = blockIdx.y, rows = A.B * A.W * A.G;
-  const int r = blockIdx.x * kMergeWarps + threadIdx.x / 32;
-  if (r >= rows) return;
-  const int tok = r / A.G, b = tok / A.W, pr = r - b * A.W * A.G;
-  const int us = kvh * A.sblocks + r / A.srows, is = r % A.srows;
+  const int grp = lane / RPB;
+  const int r = blockIdx.x * RPB + lane % RPB;
+  const bool row = r < rows;
+  const int rr = row ? r : 0;
+  const int tok = rr / A.G, b = tok / A.W, pr = rr - b * A.W * A.G;
+  const int us = kvh * A.sblocks + rr / A.srows, is = rr % A.srows;
   const int up = A.nkv * A.sblocks + (b * A.nkv + kvh) * A.pblocks + pr / A.prows;
   const int ip = pr % A.prows;
   // clamped: after a wait that expired the records may be missing
@@ -229,66 +232,59 @@ __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(SharedAr
   bs.x = max(0, min(bs.x, A.grid - 1));
   bp.x = max(0, min(bp.x, A.grid - 1));
   const int ns = seq_span(A, b, false).shared ? max(0, min(bs.y, A.grid - 1) - bs.x + 1) : 0;
-  const int n = ns + max(0, min(bp.y, A.grid - 1) - bp.x + 1);
-  float M = -INFINITY, l = 0.f, acc[N];
+  const int n = row ? ns + max(0, min(bp.y, A.grid - 1) - bp.x + 1) : 0;
+  const float2* ml_s = A.ml_s + (size_t)seg_slot(A, us, bs.x) * A.srows + is;
+  const float2* ml_p = A.ml_p + (size_t)seg_slot(A, up, bp.x) * A.prows + ip;
+  const float4* o_s = A.part_s + ((size_t)seg_slot(A, us, bs.x) * (HD / 4) + d40) * A.srows + is;
+  const float4* o_p = A.part_p + ((size_t)seg_slot(A, up, bp.x) * (HD / 4) + d40) * A.prows + ip;
+  // the row's maximum
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int i = grp; i < n; i += NG)
+    M = fmaxf(M, (i < ns ? ml_s[(size_t)i * A.srows] : ml_p[(size_t)(i - ns) * A.prows]).x);
 #pragma unroll
-  for (int k = 0; k < N; ++k) acc[k] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int i = i0 + lane;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    size_t off = 0;  // of partial i's row
-    if (i < n) {
-      off = i < ns ? (size_t)seg_slot(A, us, bs.x + i) * A.srows + is
-                   : (size_t)seg_slot(A, up, bp.x + i - ns) * A.prows + ip;
-      ml = (i < ns ? A.ml_s : A.ml_p)[off];
-    }
-    const float Mn = fmaxf(M, warp_max(ml.x));
-    if (Mn == -INFINITY) continue;
-    const float a = exp2f(M - Mn), w = exp2f(ml.x - Mn);  // 0 for -inf
-    M = Mn;
-    // a partial without keys (m = -inf) holds no O
-    l = l * a + warp_sum(ml.x == -INFINITY ? 0.f : ml.y * w);
+  for (int o = RPB; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float l = 0.f, acc[16];
 #pragma unroll
-    for (int k = 0; k < N; ++k) acc[k] *= a;
-    const unsigned live = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
-    for (int j0 = 0; j0 < 32 && i0 + j0 < n; j0 += 8) {
-      float v[8][N], wj[8];
+  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+#pragma unroll 2
+  for (int i = grp; i < n; i += NG) {
+    const bool sh = i < ns;
+    const int st = sh ? A.srows : A.prows, q = sh ? i : i - ns;
+    const float2 ml = (sh ? ml_s : ml_p)[(size_t)q * st];
+    const float4* src = (sh ? o_s : o_p) + (size_t)q * (HD / 4) * st;
+    float4 v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const size_t o = __shfl_sync(0xffffffffu, off, j0 + j);
-        wj[j] = __shfl_sync(0xffffffffu, w, j0 + j);
-        const float* src = (i0 + j0 + j < ns ? A.part_s : A.part_p) + o * HD + lane * N;
+    for (int k = 0; k < 4; ++k) v[k] = src[(size_t)k * st];
+    if (ml.x == -INFINITY) continue;  // no key seen: its O is not even written
+    const float w = exp2f(ml.x - M);
+    l = fmaf(ml.y, w, l);
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[j][k] = 0.f;
-        if (live >> (j0 + j) & 1) {
-          if constexpr (N == 4) {
-            const float4 t = *reinterpret_cast<const float4*>(src);
-            v[j][0] = t.x; v[j][1] = t.y; v[j][2] = t.z; v[j][3] = t.w;
-          } else {
-            const float2 t = *reinterpret_cast<const float2*>(src);
-            v[j][0] = t.x; v[j][1] = t.y;
-          }
-        } else {
-          wj[j] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int k = 0; k < N; ++k) acc[k] = fmaf(v[j][k], wj[j], acc[k]);
+    for (int k = 0; k < 4; ++k) {
+      acc[4 * k] = fmaf(v[k].x, w, acc[4 * k]);
+      acc[4 * k + 1] = fmaf(v[k].y, w, acc[4 * k + 1]);
+      acc[4 * k + 2] = fmaf(v[k].z, w, acc[4 * k + 2]);
+      acc[4 * k + 3] = fmaf(v[k].w, w, acc[4 * k + 3]);
     }
   }
-  const float inv = 1.f / l;  // a window row sees itself: l > 0
-  T* dst = static_cast<T*>(A.o) + ((size_t)tok * A.nkv * A.G + kvh * A.G + r % A.G) * HD + lane * N;
-  T out[N];
 #pragma unroll
-  for (int k = 0; k < N; ++k) out[k] = from_f<T>(acc[k] * inv);
-  if constexpr (sizeof(out) == 16)
-    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(out);
-  else if constexpr (sizeof(out) == 8)
-    *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(out);
-  else
-    *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(out);
+  for (int o = RPB; o < 32; o <<= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+  }
+  if (!row || grp) return;
+  const float inv = 1.f / l;  // a window row sees itself: l > 0
+  T* dst = static_cast<T*>(A.o) +
+           ((size_t)tok * A.nkv * A.G + kvh * A.G + r % A.G) * HD + d40 * 4;
+  constexpr int N = Vec16<T>::N;
+#pragma unroll
+  for (int k = 0; k < 16; k += N) {
+    Vec16<T> v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.set(i, acc[k + i] * inv);
+    st16(dst + k, v);
+  }
 }
 
 template <typename T, int HD>
@@ -303,8 +299,11 @@ cudaError_t launch_simt(const SharedArgs& A, cudaStream_t st) {
 template <typename T, int HD>
 cudaError_t launch_merge(const SharedArgs& A, cudaStream_t st) {
   const int rows = A.B * A.W * A.G;
-  return launch_pdl(shared_merge_kernel<T, HD>,
-                    dim3((rows + kMergeWarps - 1) / kMergeWarps, A.nkv), dim3(32 * kMergeWarps), 0,
+  // 8 rows a block while that leaves the GPU room, 32 (whole 512-byte runs) beyond
+  if ((long long)rows * A.nkv <= 16 * 1024)
+    return launch_pdl(shared_merge_kernel<T, HD, 8>, dim3((rows + 7) / 8, A.nkv), dim3(2 * HD), 0,
+                      st, A);
+  return launch_pdl(shared_merge_kernel<T, HD, 32>, dim3((rows + 31) / 32, A.nkv), dim3(2 * HD), 0,
                     st, A);
 }
 

@@ -24,18 +24,22 @@
 // tensor core runs them in that order, so S may follow P V into the columns that
 // P V reads.
 //
-// Code size: a unit's first and last tiles, its end and the single-thread roles
-// run code that the other warps' loops push out of the instruction caches, and
-// every line fetched again costs them hundreds of cycles (masking 128 unrolled
-// columns took 25,000 cycles).  Everything but the softmax of a full tile is
-// kept in rolled loops.
+// Code size and issue: a unit's first and last tiles, its end and the copying
+// and issuing warps run code that the softmax loops push out of the instruction
+// caches, and a line fetched again costs hundreds of cycles.  So every role is
+// one flat loop with its MMAs, copies and waits written once (with the schedule
+// inlined seven times the kernel was 140 KB, and masking a tile took 10,000
+// cycles), and only the softmax of a tile is unrolled.  Single-thread
+// instructions sit under elect.sync: under a comparison of the lane number an
+// MMA takes 90-110 cycles to issue, under elect.sync it runs at the tensor core's
+// 64 (128 x 128 x 16).
 //
-// Warps (384 threads): 0-3 softmax of A (thread = row), 4-7 of B, 8 copies Q
-// (TMA) and K/V pages (4 KiB bulk copies in the 8x8-tile operand layout, a lane
-// per page) into a ring, 9 issues the MMAs, 10 plans: it walks the split and
-// publishes the segments ahead of their use; 11 is idle.  A row's 128 scores are
-// taken in two halves of 64, the second one read from TMEM twice, so that the
-// softmax fits the 168 registers a thread has.
+// Warps (384 threads): 0-3 softmax of A (thread = row), 4-7 of B, 8 copies Q (TMA
+// boxes) and K, 11 copies V (4 KiB bulk copies of whole pages, already in the
+// 8x8-tile operand layout), 9 issues the MMAs, 10 plans: it walks the split and
+// publishes the segments ahead of their use.  A row's 128 scores are taken in two
+// halves of 64, the second one read from TMEM twice, so that the softmax fits
+// the 168 registers a thread has.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -48,7 +52,6 @@ namespace wedlm {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kRing = 4;                 // K/V tiles in shared memory
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 constexpr float kRaise = 8.f;            // log2 units
 
@@ -56,7 +59,9 @@ template <int HD> struct Cfg {
   static constexpr uint32_t kPage = kPageBlock * HD * 2;
   static constexpr uint32_t kTileBytes = kSharedTile * HD * 2;
   static constexpr uint32_t kQBytes = 128 * HD * 2;
-  static constexpr uint32_t kSmem = 2 * kQBytes + kRing * kTileBytes + 128;
+  // tiles in flight: what fits beside Q; K is needed before V
+  static constexpr int kK = HD == 128 ? 3 : 4, kV = HD == 128 ? 2 : 4;
+  static constexpr uint32_t kSmem = 2 * kQBytes + (kK + kV) * kTileBytes + 128;
 };
 
 // A segment as the planner publishes it; n = 0 ends the list.
@@ -79,37 +84,16 @@ __device__ __forceinline__ int tile_pages(const Seg& g, int t) {
   return min(kSharedTilePages, g.pages - t * kSharedTilePages);
 }
 
-// The order in which K/V tiles are used; the copier and the MMA issuer both
-// follow it.  get(seg): the next segment; on_s(x, seg, j) / on_pv(x, seg, j):
-// tile j of stream x.  Any of them ends the walk with false.
-template <typename Get, typename OnS, typename OnPV>
-__device__ __forceinline__ void run_tiles(Get get, OnS on_s, OnPV on_pv) {
-  Seg cur, nxt;
-  if (!get(cur)) return;
-  if (!on_s(0, cur, 0) || (cur.nB > 0 && !on_s(1, cur, 0))) return;
-  while (true) {
-    const bool more = get(nxt);
-#pragma unroll 1
-    for (int j = 0; j < cur.n; ++j) {
-      const bool last = j + 1 == cur.n;
-      if (!on_pv(0, cur, j)) return;
-      if (!last) {
-        if (!on_s(0, cur, j + 1)) return;
-      } else if (more) {
-        if (!on_s(0, nxt, 0)) return;
-      }
-      if (j < cur.nB && !on_pv(1, cur, j)) return;
-      if (!last) {
-        if (j + 1 < cur.nB && !on_s(1, cur, j + 1)) return;
-      } else if (more && nxt.nB > 0) {
-        if (!on_s(1, nxt, 0)) return;
-      }
-    }
-    if (!more) return;
-    cur = nxt;
-  }
+// one lane of a converged warp, known as such to the compiler
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
-
 // D[tmem] (+)= A[tmem] * B[smem desc]: A's lane is its row, each 32-bit column
 // two consecutive K elements
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
@@ -239,28 +223,33 @@ __device__ __forceinline__ void wait_st() {
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
-shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int TPB) {
+shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ SharedArgs A,
+                      int TPB) {
   using C = Cfg<HD>;
   extern __shared__ uint8_t dsm[];
-  __shared__ __align__(8) uint64_t kv_full[kRing], kv_empty[kRing], q_full[2], q_empty[2];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], fin;
-  __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], joined;
+  __shared__ __align__(8) uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV];
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
+  __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], joined, fin;
   __shared__ Seg s_seg[kSegs];
-  __shared__ int s_ids[4][kSharedTilePages];  // page ids of K tiles whose V is still to come
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_issued, s_taken, s_qissued[2], s_qtaken[2];
+  __shared__ int s_abort, s_issued[4], s_taken[4];  // copies of K, V, Q buffer 0 and 1
   __shared__ float2 s_ml[2][128];
 
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 127) &
                                              ~static_cast<uintptr_t>(127));
-  uint8_t* ring = base + 2 * C::kQBytes;
+  uint8_t* k_ring = base + 2 * C::kQBytes;
+  uint8_t* v_ring = k_ring + C::kK * C::kTileBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = A.G;
 
   if (threadIdx.x == 32) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < C::kK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::kV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
@@ -268,15 +257,15 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
       mbar_init(&pv_done[x], 1);
-      s_qissued[x] = s_qtaken[x] = 0;
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 10);  // copier, issuer, 8 softmax warps
+      mbar_init(&seg_empty[i], 11);  // two copiers, issuer, 8 softmax warps
+      s_issued[i] = s_taken[i] = 0;
     }
     mbar_init(&joined, 8);
     mbar_init(&fin, 1);
-    s_abort = s_issued = s_taken = 0;
+    s_abort = 0;
     mbar_fence_init();
   }
   if (warp == 0) {
@@ -288,17 +277,24 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort = &s_abort;
-  // warp-wide and bounded: what follows is executed by the whole warp together
+  // warp-wide and bounded (2 s): what follows is executed by the whole warp together
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     bool ok = mbar_try_wait(bar, parity);
-    if (!ok && !*abort) {
-      ok = mbar_wait(bar, parity, A.err);
-      if (!ok) *abort = 1;
+    if (!ok) {
+      uint64_t t0 = 0;
+#pragma unroll 1
+      for (int n = 1; !(ok = mbar_try_wait(bar, parity)) && !*abort; ++n) {
+        if (n & 4095) continue;
+        if (!t0) t0 = global_ns();
+        if (global_ns() - t0 > kWaitNs) {
+          set_err(A.err, WEDLM_DEV_TIMEOUT);
+          *abort = 1;
+        }
+      }
     }
     return __all_sync(0xffffffffu, ok);
   };
-
-  // next published segment, into registers (warp-wide)
+  // next published segment, into registers (warp-wide); false after the last
   int seg_i = 0;
   uint32_t seg_ph = 0;
   auto get = [&](Seg& g) -> bool {
@@ -315,13 +311,13 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
 
   pdl_wait();  // nothing of an earlier kernel is read before
   pdl_trigger();
-  if (warp >= 8) {
-    if (warp == 10) {
+  if (warp == 10) {
     // ---------------- planner ----------------
     SharedWalk walk;
     walk.init(A);
     SharedSeg u;
     bool more;
+#pragma unroll 1
     do {
       more = __shfl_sync(0xffffffffu, walk.next(A, u), 0);
       Seg g = {};
@@ -361,199 +357,197 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
         seg_ph ^= 1u;
       }
     } while (more);
-    } else
-    if (warp == 8) {
-    // ---------------- copier ----------------
-    if (lane == 0) tma_prefetch_desc(&mq);
+  } else if (warp == 8 || warp == 11) {
+    // ---------------- copiers: Q and K (8), V (11) ----------------
+    const int kv = warp == 11;
+    const int NS = kv ? C::kV : C::kK;
+    uint64_t* full = kv ? v_full : k_full;
+    uint64_t* empty = kv ? v_empty : k_empty;
+    uint8_t* ring = kv ? v_ring : k_ring;
     const uint64_t keep = l2_evict_last_policy(), once = l2_evict_first_policy();
-    int st = 0;
+    if (!kv && elect_one()) tma_prefetch_desc(&mq);
+    int st = 0, issued = 0, nq0 = 0, nq1 = 0, flip = 0;
     uint32_t ph = 0;
-    int issued = 0, flip = 0, nq[2] = {0, 0};
-    // this lane's page id of the next K tile, loaded a tile ahead
-    int next_id = -1, nk = 0, nv = 0;
+    // this lane's page id of a tile, loaded a tile ahead of its use
     auto id_of = [&](const Seg& g, int t) -> int {
       const int j = t * kSharedTilePages + lane;
       return lane < kSharedTilePages && t < g.t1 && j < (g.b < 0 ? g.pages : g.n_own)
                  ? own_page_id(A, g.b, g.shared, j)
                  : -1;
     };
-    auto load_tile = [&](const Seg& g, int t, int kv) -> bool {
-      const int np = tile_pages(g, t), j = t * kSharedTilePages + lane;
-      int id = -1;
-      if (kv == 0) {
-        id = next_id;
-        if (lane < kSharedTilePages) s_ids[nk & 3][lane] = id;
-        ++nk;
-        next_id = id_of(g, t + 1);
-      } else {  // V tiles follow in the order of the K tiles, at most 3 behind
-        if (lane < kSharedTilePages) id = s_ids[nv & 3][lane];
-        ++nv;
-      }
-      const bf16* src = nullptr;
-      if (lane < np) {
-        if (g.b >= 0 && j >= g.n_own)
-          src = window_block<bf16>(A, g.b, j - g.n_own, kv, g.kvh, HD);
-        else if (id >= 0 && id < A.num_pages)
-          src = cached_block<bf16>(A, id, kv, g.kvh, HD);
-        else
-          set_err(A.err, WEDLM_DEV_BAD_PAGE);
-      }
-      if (!wait(&kv_empty[st], ph ^ 1u)) return false;
-      uint8_t* dst = ring + st * C::kTileBytes;
-      const unsigned missing = __ballot_sync(0xffffffffu, lane < np && !src);
-      if (missing) {  // page ids out of range read as zeros
-        for (int p = 0; p < np; ++p)
-          if (missing >> p & 1)
-            for (int e = lane; e < (int)C::kPage / 16; e += 32)
-              reinterpret_cast<uint4*>(dst + p * C::kPage)[e] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+    Seg g;
+    bool ok = get(g);
+    int next_id = ok ? id_of(g, g.t0) : -1;
+    while (ok) {
+      // Q: A's and B's row block, or one buffer in turn for both
+#pragma unroll 1
+      for (int x = 0; ok && !kv && x < 1 + g.pair; ++x) {
+        const int buf = g.pair ? x : flip;
+        const int nq = buf ? nq1++ : nq0++;
+        if (!wait(&q_empty[buf], (uint32_t)(nq & 1) ^ 1u)) ok = false;
+        if (ok && elect_one()) {
+          mbar_arrive_expect_tx(&q_full[buf], (uint32_t)(min(TPB, A.B * A.W) * G) * HD * 2);
+#pragma unroll 1
+          for (int c = 0; c < HD / 8; ++c)
+            load_q_box(base + buf * C::kQBytes + c * 2048, &mq, &q_full[buf], 8 * c, g.kvh * G,
+                       g.tok0 + x * TPB);
+          s_issued[2 + buf] = nq + 1;
+        }
         __syncwarp();
       }
-      if (lane == 0)
-        mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(np - __popc(missing)) * C::kPage);
-      __syncwarp();
-      if (lane < np && src)
-        bulk_load(dst + lane * C::kPage, src, C::kPage, &kv_full[st], g.b < 0 ? keep : once);
-      if (lane == 0) s_issued = ++issued;
-      if (++st == kRing) {
-        st = 0;
-        ph ^= 1u;
-      }
-      return true;
-    };
-    auto load_q = [&](const Seg& g, int buf, int tok) -> bool {
-      if (!wait(&q_empty[buf], (uint32_t)(nq[buf] & 1) ^ 1u)) return false;
-      ++nq[buf];
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full[buf], (uint32_t)(min(TPB, A.B * A.W) * G) * HD * 2);
+      if (!g.pair) flip ^= 1;
+      Seg nxt;
+      const bool more = ok && get(nxt);
 #pragma unroll 1
-        for (int c = 0; c < HD / 8; ++c)
-          load_q_box(base + buf * C::kQBytes + c * 2048, &mq, &q_full[buf], 8 * c, g.kvh * G, tok);
-        s_qissued[buf] = nq[buf];
+      for (int t = g.t0; ok && t < g.t1; ++t) {
+        const int np = tile_pages(g, t), j = t * kSharedTilePages + lane;
+        const int id = next_id;
+        next_id = t + 1 < g.t1 ? id_of(g, t + 1) : more ? id_of(nxt, nxt.t0) : -1;
+        const bf16* src = nullptr;
+        if (lane < np) {
+          if (g.b >= 0 && j >= g.n_own)
+            src = window_block<bf16>(A, g.b, j - g.n_own, kv, g.kvh, HD);
+          else if (id >= 0 && id < A.num_pages)
+            src = cached_block<bf16>(A, id, kv, g.kvh, HD);
+          else
+            set_err(A.err, WEDLM_DEV_BAD_PAGE);
+        }
+        if (!wait(&empty[st], ph ^ 1u)) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = ring + st * C::kTileBytes;
+        const unsigned have = __ballot_sync(0xffffffffu, src != nullptr);
+        if (__popc(have) < np) {  // page ids out of range read as zeros
+          for (int p = 0; p < np; ++p)
+            if (!(have >> p & 1))
+              for (int e = lane; e < (int)C::kPage / 16; e += 32)
+                reinterpret_cast<uint4*>(dst + p * C::kPage)[e] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const bool one = elect_one();
+        if (one) mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(have) * C::kPage);
+#pragma unroll 1
+        for (int p = 0; p < np; ++p) {
+          const bf16* s =
+              reinterpret_cast<const bf16*>(__shfl_sync(0xffffffffu, (unsigned long long)src, p));
+          if (one && s) bulk_load(dst + p * C::kPage, s, C::kPage, &full[st], g.b < 0 ? keep : once);
+        }
+        if (one) s_issued[kv] = ++issued;
+        __syncwarp();
+        if (++st == NS) {
+          st = 0;
+          ph ^= 1u;
+        }
       }
-      return true;
-    };
-    run_tiles(
-        [&](Seg& g) -> bool { return get(g); },
-        [&](int x, const Seg& g, int j) -> bool {
-          if (j == 0) {
-            if (x == 0) next_id = id_of(g, g.t0);
-            if (g.pair) {
-              if (!load_q(g, x, g.tok0 + x * TPB)) return false;
-            } else if (x == 0) {
-              if (!load_q(g, flip, g.tok0)) return false;
-              flip ^= 1;
-            }
-          }
-          return (g.pair && x == 1) || load_tile(g, seg_tile(g, x, j), 0);
-        },
-        [&](int x, const Seg& g, int j) -> bool {
-          return (g.pair && x == 1) || load_tile(g, seg_tile(g, x, j), 1);
-        });
-    } else if (warp == 9) {
+      if (!more) break;
+      g = nxt;
+    }
+  } else if (warp == 9) {
     // ---------------- MMA issuer ----------------
+    // Step r is tile j of a segment, for both streams.  Round r: P V of step r-1
+    // and S of step r for A, then for B.
     // Q: 8-dim groups 2048 B apart, 8-row groups 128 B; K: 128 B and HD*16 B
     // (K-major); V: 8-token groups HD*16 B apart, 8-dim groups 128 B (MN-major)
     const uint64_t dq0 = sdesc_noswz(smem_u32(base), 2048, 128);
-    const uint64_t dk0 = sdesc_noswz(smem_u32(ring), 128, HD * 16);
-    const uint64_t dv0 = sdesc_noswz(smem_u32(ring), HD * 16, 128);
+    const uint64_t dk0 = sdesc_noswz(smem_u32(k_ring), 128, HD * 16);
+    const uint64_t dv0 = sdesc_noswz(smem_u32(v_ring), HD * 16, 128);
     const uint32_t idPV = idesc_bf16_m128(HD) | (1u << 16);
-    int st = 0, kst = 0, vst = 0, taken = 0, flip = 0, nq[2] = {0, 0}, qbuf = 0;
-    uint32_t ph = 0, pph[2] = {0, 0};
-    auto take = [&](int& slot) -> bool {
-      if (!wait(&kv_full[st], ph)) return false;
-      slot = st;
-      if (lane == 0) s_taken = ++taken;
-      if (++st == kRing) {
-        st = 0;
-        ph ^= 1u;
-      }
-      return true;
-    };
-    auto take_q = [&](int buf) -> bool {
-      if (!wait(&q_full[buf], (uint32_t)(nq[buf] & 1))) return false;
-      ++nq[buf];
-      if (lane == 0) s_qtaken[buf] = nq[buf];
-      return true;
-    };
-    run_tiles(
-        [&](Seg& g) -> bool { return get(g); },
-        [&](int x, const Seg& g, int j) -> bool {
-          if (j == 0) {
-            if (g.pair) {
-              if (!take_q(x)) return false;
-            } else if (x == 0) {
-              qbuf = flip;
-              flip ^= 1;
-              if (!take_q(qbuf)) return false;
-            }
-          }
-          if (!(g.pair && x == 1) && !take(kst)) return false;
-          if (lane == 0) {
-            tc_fence_after();
-            const int buf = g.pair ? x : qbuf;
-            const uint64_t dq = dq0 + (uint64_t)(buf * C::kQBytes >> 4);
-            const uint64_t dk = dk0 + (uint64_t)(kst * C::kTileBytes >> 4);
-            const uint32_t id =
-                idesc_bf16_m128(tile_pages(g, seg_tile(g, x, j)) * kPageBlock);
-            const uint32_t d = tmem + kColS + (uint32_t)(x * 128);
-#pragma unroll 1  // rolled: see the note on code size
-            for (int k = 0; k < HD / 16; ++k)  // 16 dims: two 8-dim groups
-              tc_mma_f16(d, dq + k * 256, dk + k * 16, id, k ? 1u : 0u);
-            tc_commit(&s_full[x]);
-            if (!g.pair || x == 1) tc_commit(&kv_empty[kst]);
-            const int nx = x ? g.nB : g.n;
-            if (g.pair ? j + 1 == nx : seg_tile(g, x, j) + 1 == g.t1) tc_commit(&q_empty[buf]);
-          }
-          __syncwarp();
-          return true;
-        },
-        [&](int x, const Seg& g, int j) -> bool {
-          const int t = seg_tile(g, x, j), np = tile_pages(g, t);
-          if (!(g.pair && x == 1)) {
-            if (!take(vst)) return false;
+    int kst = C::kK - 1, vst = C::kV - 1, nk = 0, nv = 0, nq0 = 0, nq1 = 0, qbuf = 0, flip = 0;
+    uint32_t kph = 1, vph = 1, pph0 = 0, pph1 = 0;  // of the tile held
+    Seg cur, prev;
+    int j = 0, pj = 0;
+    bool have = get(cur), held = false, ok = true;
+#pragma unroll 1
+    while (ok && (have || held)) {
+#pragma unroll 1
+      for (int x = 0; ok && x < 2; ++x) {
+        if (held && (x == 0 || pj < prev.nB)) {
+          const int t = seg_tile(prev, x, pj), np = tile_pages(prev, t);
+          if (x == 0 || !prev.pair) {
+            if (++vst == C::kV) vst = 0;
+            if (vst == 0) vph ^= 1u;
+            if (!(ok = wait(&v_full[vst], vph))) break;
+            s_taken[1] = ++nv;
             // V rows that no query sees (the tails of the last cached page and of
             // the window) become zeros: 0 * NaN would reach every row
-            const int c_own = g.own_keys - t * kSharedTile;        // cached keys in this tile
-            const int c_win = g.n_own * kPageBlock - t * kSharedTile + A.W;  // window end
-            if (g.b >= 0 && ((c_own > 0 && c_own < kSharedTile && (c_own & 15)) ||
-                             (c_win > 0 && c_win < kSharedTile && (c_win & 15)))) {
-              for (int part = 0; part < 2; ++part) {
-                const int c = part ? c_win : c_own;
-                if (c <= 0 || c >= kSharedTile || !(c & 15)) continue;
-                const int rows = 16 - (c & 15);
-                for (int e = lane; e < rows * (HD / 8); e += 32)
-                  *reinterpret_cast<uint4*>(ring + vst * C::kTileBytes +
-                                            2 * ((c >> 4) * kPageBlock * HD +
-                                                 tile_off((c & 15) + e % rows, e / rows * 8, HD))) =
-                      make_uint4(0, 0, 0, 0);
-              }
+            const int c_own = prev.own_keys - t * kSharedTile;  // cached keys of this tile
+            const int c_win = prev.n_own * kPageBlock - t * kSharedTile + A.W;  // window's end
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part) {
+              const int c = part ? c_win : c_own;
+              if (prev.b < 0 || c <= 0 || c >= kSharedTile || !(c & 15)) continue;
+              const int rows = 16 - (c & 15);
+#pragma unroll 1
+              for (int e = lane; e < rows * (HD / 8); e += 32)
+                *reinterpret_cast<uint4*>(v_ring + vst * C::kTileBytes +
+                                          2 * ((c >> 4) * kPageBlock * HD +
+                                               tile_off((c & 15) + e % rows, e / rows * 8, HD))) =
+                    make_uint4(0, 0, 0, 0);
               fence_proxy_async_smem();
-              __syncwarp();
             }
+            __syncwarp();
           }
-          if (!wait(&p_full[x], pph[x])) return false;
-          pph[x] ^= 1u;
-          if (lane == 0) {
+          if (!(ok = wait(&p_full[x], x ? pph1 : pph0))) break;
+          if (x) pph1 ^= 1u; else pph0 ^= 1u;
+          if (elect_one()) {
             tc_fence_after();
             const uint64_t dv = dv0 + (uint64_t)(vst * C::kTileBytes >> 4);
             const uint32_t d = tmem + kColO + (uint32_t)(x * 128);
             const uint32_t p = tmem + kColS + (uint32_t)(x * 128);
-#pragma unroll 1
-            for (int k = 0; k < np; ++k)  // 16 keys: 8 columns of P
-              mma_ts(d, p + k * 8, dv + k * (HD * 2), idPV, (j || k) ? 1u : 0u);
+#pragma unroll
+            for (int k = 0; k < kSharedTilePages; ++k)  // 16 keys: 8 columns of P
+              if (k < np) mma_ts(d, p + k * 8, dv + k * (HD * 2), idPV, (pj || k) ? 1u : 0u);
             tc_commit(&pv_done[x]);
-            if (!g.pair || x == 1) tc_commit(&kv_empty[vst]);
+            if (x == 1 || !prev.pair) tc_commit(&v_empty[vst]);
           }
           __syncwarp();
-          return true;
-        });
+        }
+        if (have && (x == 0 || j < cur.nB)) {
+          const int t = seg_tile(cur, x, j), np = tile_pages(cur, t);
+          if (j == 0 && (cur.pair || x == 0)) {  // a new segment's Q
+            qbuf = cur.pair ? x : flip;
+            if (!cur.pair) flip ^= 1;
+            const int nq = qbuf ? nq1++ : nq0++;
+            if (!(ok = wait(&q_full[qbuf], (uint32_t)(nq & 1)))) break;
+            s_taken[2 + qbuf] = nq + 1;
+          }
+          if (x == 0 || !cur.pair) {
+            if (++kst == C::kK) kst = 0;
+            if (kst == 0) kph ^= 1u;
+            if (!(ok = wait(&k_full[kst], kph))) break;
+            s_taken[0] = ++nk;
+          }
+          const int buf = cur.pair ? x : qbuf;
+          if (elect_one()) {
+            tc_fence_after();
+            const uint64_t dq = dq0 + (uint64_t)(buf * C::kQBytes >> 4);
+            const uint64_t dk = dk0 + (uint64_t)(kst * C::kTileBytes >> 4);
+            const uint32_t id = idesc_bf16_m128(np * kPageBlock);
+            const uint32_t d = tmem + kColS + (uint32_t)(x * 128);
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)  // 16 dims: two 8-dim groups
+              tc_mma_f16(d, dq + k * 256, dk + k * 16, id, k ? 1u : 0u);
+            tc_commit(&s_full[x]);
+            if (x == 1 || !cur.pair) tc_commit(&k_empty[kst]);
+            // the last S of the segment from this Q
+            if (cur.pair ? j + 1 == cur.n : t + 1 == cur.t1) tc_commit(&q_empty[buf]);
+          }
+          __syncwarp();
+        }
+      }
+      held = have;
+      prev = cur;
+      pj = j;
+      if (have && ++j == cur.n) {
+        j = 0;
+        have = get(cur);
+      }
+    }
     // every MMA has completed before TMEM is freed
-    if (lane == 0) {
-      tc_commit(&fin);
-      mbar_wait(&fin, 0, A.err);
-    }
-    }
+    if (elect_one()) tc_commit(&fin);
+    mbar_wait(&fin, 0, A.err);
   } else {
     // ---------------- softmax ----------------
     const int x = warp >> 2;                       // stream
@@ -644,7 +638,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
       if (nx > 0) wait(&pv_done[x], dph ^ 1u);
       tc_fence_after();
       const int urows = g.b < 0 ? A.srows : A.prows;
-      float* po = (g.b < 0 ? A.part_s : A.part_p) + (size_t)g.slot * urows * HD;
+      float4* po = (g.b < 0 ? A.part_s : A.part_p) + (size_t)g.slot * urows * (HD / 4);
       float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + (size_t)g.slot * urows;
       if (g.pair) {
         const int row = x * TPB * G + r;
@@ -654,7 +648,9 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
           ld32(tO + c, o);
           if (valid)
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) st_sector(po + (size_t)row * HD + c + k, o + k);
+            for (int k = 0; k < 8; ++k)
+              po[(size_t)(c / 4 + k) * urows + row] =
+                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
         if (valid) ml[row] = make_float2(m, l);
         tc_fence_before();
@@ -684,8 +680,9 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
           }
           if (valid)
 #pragma unroll
-            for (int k = 0; k < 32; k += 8)
-              st_sector(po + (size_t)r * HD + x * (HD / 2) + c + k, o + k);
+            for (int k = 0; k < 8; ++k)
+              po[(size_t)((x * (HD / 2) + c) / 4 + k) * urows + r] =
+                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
         if (valid && x == 0) ml[r] = make_float2(M, l * am + o_ml.y * ao);
         tc_fence_before();
@@ -698,10 +695,12 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, SharedArgs A, int 
   tc_fence_after();
   if (s_abort && threadIdx.x == 256) {
     // a wait expired: let the copies still in flight land (bounded)
-    for (int i = s_taken; i < s_issued; ++i)
-      mbar_wait(&kv_full[i % kRing], (uint32_t)(i / kRing) & 1u, A.err);
+    for (int i = s_taken[0]; i < s_issued[0]; ++i)
+      mbar_wait(&k_full[i % C::kK], (uint32_t)(i / C::kK) & 1u, A.err);
+    for (int i = s_taken[1]; i < s_issued[1]; ++i)
+      mbar_wait(&v_full[i % C::kV], (uint32_t)(i / C::kV) & 1u, A.err);
     for (int x = 0; x < 2; ++x)
-      for (int i = s_qtaken[x]; i < s_qissued[x]; ++i)
+      for (int i = s_taken[2 + x]; i < s_issued[2 + x]; ++i)
         mbar_wait(&q_full[x], (uint32_t)i & 1u, A.err);
   }
   __syncthreads();

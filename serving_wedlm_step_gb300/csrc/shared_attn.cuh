@@ -40,7 +40,7 @@ struct SharedArgs {
   int ucost, shared_cost, private_cost, min_share;
   int grid;
   // workspace
-  float *part_s, *part_p;         // [slot][rows of a unit][hd] partial O
+  float4 *part_s, *part_p;        // [slot][hd/4][rows of a unit] partial O
   float2 *ml_s, *ml_p;            // [slot][rows of a unit] running max (log2 units), row sum
   int2* unit_blocks;              // [unit] blocks of the first and last tile
 };
@@ -185,13 +185,6 @@ struct SharedWalk {
 __device__ __forceinline__ int seg_slot(const SharedArgs& A, int unit, int block) {
   const int ns = A.nkv * A.sblocks;
   return (unit < ns ? unit : unit - ns) + block;
-}
-
-// 8 floats to one 32-byte sector
-__device__ __forceinline__ void st_sector(float* p, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
-               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
 }
 
 // one thread of the block records the unit's first and last block
