@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(2 * HD) shared_merge_kernel(const __grid_const
   int2 bs = A.unit_blocks[us], bp = A.unit_blocks[up];
   bs.x = max(0, min(bs.x, A.grid - 1));
   bp.x = max(0, min(bp.x, A.grid - 1));
-  const int ns = seq_span(A, b, false).shared ? max(0, min(bs.y, A.grid - 1) - bs.x + 1) : 0;
+  const int ns = seq_span(A, b).shared ? max(0, min(bs.y, A.grid - 1) - bs.x + 1) : 0;
   const int n = row ? ns + max(0, min(bp.y, A.grid - 1) - bp.x + 1) : 0;
   const float2* ml_s = A.ml_s + (size_t)seg_slot(A, us, bs.x) * A.srows + is;
   const float2* ml_p = A.ml_p + (size_t)seg_slot(A, up, bp.x) * A.prows + ip;

@@ -20,26 +20,27 @@
 // stale one, which the division by l (held in 32 bits, like m and O) undoes.
 //
 // TMEM (512 columns): S/P of A at 0, of B at 128, O of A at 256, of B at 384.
-// One thread issues every MMA, in the order A: P V, next S; B: P V, next S; the
-// tensor core runs them in that order, so S may follow P V into the columns that
-// P V reads.
+// Each stream has its own issuing warp: P V of one tile, then S of the next, back
+// to back.  The tensor core takes a thread's MMAs in order, so S may follow P V
+// into the columns that P V reads; and its queue is short, so what one issuer
+// spends on waits and descriptors is time the other's MMAs run.
 //
-// Code size and issue: a unit's first and last tiles, its end and the copying
-// and issuing warps run code that the softmax loops push out of the instruction
-// caches, and a line fetched again costs hundreds of cycles.  So every role is
-// one flat loop with its MMAs, copies and waits written once (with the schedule
-// inlined seven times the kernel was 140 KB, and masking a tile took 10,000
-// cycles), and only the softmax of a tile is unrolled.  Single-thread
-// instructions sit under elect.sync: under a comparison of the lane number an
-// MMA takes 90-110 cycles to issue, under elect.sync it runs at the tensor core's
-// 64 (128 x 128 x 16).
+// Single-thread instructions sit under elect.sync: under a comparison of the lane
+// number an MMA took 90-110 cycles to issue, under elect.sync it runs at the
+// tensor core's 64 (128 x 128 x 16).
+//
+// Code size: an SM holds about 64 KB of instructions; beyond that a 128-byte line
+// costs 1300 cycles (measured with straight-line code).  An unrolled schedule made
+// this kernel 140 KB, and masking one tile took 10,000 cycles.  So every role is a
+// flat loop with its MMAs, copies and waits written once, and only the softmax of
+// a tile is unrolled.
 //
 // Warps (384 threads): 0-3 softmax of A (thread = row), 4-7 of B, 8 copies Q (TMA
-// boxes) and K, 11 copies V (4 KiB bulk copies of whole pages, already in the
-// 8x8-tile operand layout), 9 issues the MMAs, 10 plans: it walks the split and
-// publishes the segments ahead of their use.  A row's 128 scores are taken in two
-// halves of 64, the second one read from TMEM twice, so that the softmax fits
-// the 168 registers a thread has.
+// boxes), K and V (4 KiB bulk copies of whole pages, already in the 8x8-tile
+// operand layout), 9 and 11 issue the MMAs of A and B, 10 plans: it walks the
+// split and publishes the segments ahead of their use.  A row's 128 scores are
+// taken in two halves of 64, the second one read from TMEM twice, so that the
+// softmax fits the 168 registers a thread has.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -221,6 +222,24 @@ __device__ __forceinline__ void wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// the slow half of a wait, written once; false when this or another wait expired
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err,
+                                     volatile int* abort) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (int n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if (*abort) return false;
+    if (n & 4095) continue;
+    if (!t0) t0 = global_ns();
+    if (global_ns() - t0 > kWaitNs) {
+      set_err(err, WEDLM_DEV_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ SharedArgs A,
@@ -232,7 +251,9 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], joined, fin;
   __shared__ Seg s_seg[kSegs];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_issued[4], s_taken[4];  // copies of K, V, Q buffer 0 and 1
+  __shared__ int s_abort, s_issued[4];  // copies of K, V, Q buffer 0 and 1 started
+  __shared__ const bf16* s_src[kSharedTilePages];
+  __shared__ int s_ids[4][kSharedTilePages];  // page ids of K tiles whose V is to come
   __shared__ float2 s_ml[2][128];
 
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 127) &
@@ -245,26 +266,26 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   if (threadIdx.x == 32) {
     for (int i = 0; i < C::kK; ++i) {
       mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&k_empty[i], 2);  // both issuers, or one of them twice
     }
     for (int i = 0; i < C::kV; ++i) {
       mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_empty[i], 2);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
-      mbar_init(&q_empty[x], 1);
+      mbar_init(&q_empty[x], 2);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
       mbar_init(&pv_done[x], 1);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 11);  // two copiers, issuer, 8 softmax warps
-      s_issued[i] = s_taken[i] = 0;
+      mbar_init(&seg_empty[i], 11);  // copier, issuers, 8 softmax warps
+      s_issued[i] = 0;
     }
     mbar_init(&joined, 8);
-    mbar_init(&fin, 1);
+    mbar_init(&fin, 2);
     s_abort = 0;
     mbar_fence_init();
   }
@@ -276,22 +297,10 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  volatile int* abort = &s_abort;
   // warp-wide and bounded (2 s): what follows is executed by the whole warp together
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-      uint64_t t0 = 0;
-#pragma unroll 1
-      for (int n = 1; !(ok = mbar_try_wait(bar, parity)) && !*abort; ++n) {
-        if (n & 4095) continue;
-        if (!t0) t0 = global_ns();
-        if (global_ns() - t0 > kWaitNs) {
-          set_err(A.err, WEDLM_DEV_TIMEOUT);
-          *abort = 1;
-        }
-      }
-    }
+    if (!ok) ok = wait_on(bar, parity, A.err, &s_abort);
     return __all_sync(0xffffffffu, ok);
   };
   // next published segment, into registers (warp-wide); false after the last
@@ -357,18 +366,12 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         seg_ph ^= 1u;
       }
     } while (more);
-  } else if (warp == 8 || warp == 11) {
-    // ---------------- copiers: Q and K (8), V (11) ----------------
-    const int kv = warp == 11;
-    const int NS = kv ? C::kV : C::kK;
-    uint64_t* full = kv ? v_full : k_full;
-    uint64_t* empty = kv ? v_empty : k_empty;
-    uint8_t* ring = kv ? v_ring : k_ring;
+  } else if (warp == 8) {
+    // ---------------- copier ----------------
     const uint64_t keep = l2_evict_last_policy(), once = l2_evict_first_policy();
-    if (!kv && elect_one()) tma_prefetch_desc(&mq);
-    int st = 0, issued = 0, nq0 = 0, nq1 = 0, flip = 0;
-    uint32_t ph = 0;
-    // this lane's page id of a tile, loaded a tile ahead of its use
+    if (elect_one()) tma_prefetch_desc(&mq);
+    int nk = 0, nv = 0, nq0 = 0, nq1 = 0, flip = 0;
+    // this lane's page id of a K tile, loaded a tile ahead of its use
     auto id_of = [&](const Seg& g, int t) -> int {
       const int j = t * kSharedTilePages + lane;
       return lane < kSharedTilePages && t < g.t1 && j < (g.b < 0 ? g.pages : g.n_own)
@@ -378,14 +381,15 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     Seg g;
     bool ok = get(g);
     int next_id = ok ? id_of(g, g.t0) : -1;
+#pragma unroll 1
     while (ok) {
       // Q: A's and B's row block, or one buffer in turn for both
 #pragma unroll 1
-      for (int x = 0; ok && !kv && x < 1 + g.pair; ++x) {
+      for (int x = 0; x < 1 + g.pair; ++x) {
         const int buf = g.pair ? x : flip;
         const int nq = buf ? nq1++ : nq0++;
-        if (!wait(&q_empty[buf], (uint32_t)(nq & 1) ^ 1u)) ok = false;
-        if (ok && elect_one()) {
+        if (!(ok = wait(&q_empty[buf], (uint32_t)(nq & 1) ^ 1u))) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&q_full[buf], (uint32_t)(min(TPB, A.B * A.W) * G) * HD * 2);
 #pragma unroll 1
           for (int c = 0; c < HD / 8; ++c)
@@ -398,11 +402,22 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       if (!g.pair) flip ^= 1;
       Seg nxt;
       const bool more = ok && get(nxt);
+      // K0, K1, V0, K2, V1, .. , V of the last
+      const int T = g.t1 - g.t0;
 #pragma unroll 1
-      for (int t = g.t0; ok && t < g.t1; ++t) {
+      for (int i = 0; ok && i < 2 * T; ++i) {
+        const int m = (i + 1) >> 1;
+        const int kv = i > 0 && (!(i & 1) || m == T);
+        const int t = g.t0 + (!kv ? m : i & 1 ? T - 1 : (i >> 1) - 1);
         const int np = tile_pages(g, t), j = t * kSharedTilePages + lane;
-        const int id = next_id;
-        next_id = t + 1 < g.t1 ? id_of(g, t + 1) : more ? id_of(nxt, nxt.t0) : -1;
+        int id = next_id;
+        const int n = kv ? nv++ : nk++;
+        if (kv) {
+          id = s_ids[n & 3][lane & 7];  // V follows in K's order, at most 3 behind
+        } else {
+          if (lane < kSharedTilePages) s_ids[n & 3][lane] = id;
+          next_id = t + 1 < g.t1 ? id_of(g, t + 1) : more ? id_of(nxt, nxt.t0) : -1;
+        }
         const bf16* src = nullptr;
         if (lane < np) {
           if (g.b >= 0 && j >= g.n_own)
@@ -412,138 +427,138 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           else
             set_err(A.err, WEDLM_DEV_BAD_PAGE);
         }
-        if (!wait(&empty[st], ph ^ 1u)) {
-          ok = false;
-          break;
-        }
-        uint8_t* dst = ring + st * C::kTileBytes;
         const unsigned have = __ballot_sync(0xffffffffu, src != nullptr);
+        if (lane < kSharedTilePages) s_src[lane] = src;
+        const int NS = kv ? C::kV : C::kK, use = n / NS, st = n - use * NS;
+        uint64_t* full = (kv ? v_full : k_full) + st;
+        if (!(ok = wait((kv ? v_empty : k_empty) + st, (uint32_t)(use & 1) ^ 1u))) break;
+        uint8_t* dst = (kv ? v_ring : k_ring) + st * C::kTileBytes;
         if (__popc(have) < np) {  // page ids out of range read as zeros
-          for (int p = 0; p < np; ++p)
-            if (!(have >> p & 1))
-              for (int e = lane; e < (int)C::kPage / 16; e += 32)
-                reinterpret_cast<uint4*>(dst + p * C::kPage)[e] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+          for (int e = lane; e < np * (int)C::kPage / 16; e += 32)
+            if (!(have >> (e / (C::kPage / 16)) & 1))
+              reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const bool one = elect_one();
-        if (one) mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(have) * C::kPage);
-#pragma unroll 1
-        for (int p = 0; p < np; ++p) {
-          const bf16* s =
-              reinterpret_cast<const bf16*>(__shfl_sync(0xffffffffu, (unsigned long long)src, p));
-          if (one && s) bulk_load(dst + p * C::kPage, s, C::kPage, &full[st], g.b < 0 ? keep : once);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full, (uint32_t)__popc(have) * C::kPage);
+          const uint64_t pol = g.b < 0 ? keep : once;
+#pragma unroll
+          for (int p = 0; p < kSharedTilePages; ++p)
+            if (have >> p & 1) bulk_load(dst + p * C::kPage, s_src[p], C::kPage, full, pol);
+          s_issued[kv] = n + 1;
         }
-        if (one) s_issued[kv] = ++issued;
         __syncwarp();
-        if (++st == NS) {
-          st = 0;
-          ph ^= 1u;
-        }
       }
       if (!more) break;
       g = nxt;
     }
-  } else if (warp == 9) {
-    // ---------------- MMA issuer ----------------
-    // Step r is tile j of a segment, for both streams.  Round r: P V of step r-1
-    // and S of step r for A, then for B.
+  } else if (warp == 9 || warp == 11) {
+    // ---------------- MMA issuers ----------------
     // Q: 8-dim groups 2048 B apart, 8-row groups 128 B; K: 128 B and HD*16 B
     // (K-major); V: 8-token groups HD*16 B apart, 8-dim groups 128 B (MN-major)
+    const int x = warp == 11;
     const uint64_t dq0 = sdesc_noswz(smem_u32(base), 2048, 128);
     const uint64_t dk0 = sdesc_noswz(smem_u32(k_ring), 128, HD * 16);
     const uint64_t dv0 = sdesc_noswz(smem_u32(v_ring), HD * 16, 128);
     const uint32_t idPV = idesc_bf16_m128(HD) | (1u << 16);
-    int kst = C::kK - 1, vst = C::kV - 1, nk = 0, nv = 0, nq0 = 0, nq1 = 0, qbuf = 0, flip = 0;
-    uint32_t kph = 1, vph = 1, pph0 = 0, pph1 = 0;  // of the tile held
-    Seg cur, prev;
-    int j = 0, pj = 0;
-    bool have = get(cur), held = false, ok = true;
+    const uint32_t dS = tmem + kColS + (uint32_t)(x * 128), dO = tmem + kColO + (uint32_t)(x * 128);
+    Seg g;
+    int j = -1;             // tile of this stream in the segment
+    int base_n = 0;         // tiles of the block before the segment
+    int nq0 = 0, nq1 = 0, flip = 0;
+    // the tile whose P V is due: its number, pages, whether O starts with it, the
+    // ends of its cached keys and of the window in it
+    int pn = -1, pnp = 0, pfirst = 0, pc0 = 0, pc1 = 0, ppair = 0;
+    uint32_t pph = 0;
+    bool have = get(g), ok = true;
 #pragma unroll 1
-    while (ok && (have || held)) {
-#pragma unroll 1
-      for (int x = 0; ok && x < 2; ++x) {
-        if (held && (x == 0 || pj < prev.nB)) {
-          const int t = seg_tile(prev, x, pj), np = tile_pages(prev, t);
-          if (x == 0 || !prev.pair) {
-            if (++vst == C::kV) vst = 0;
-            if (vst == 0) vph ^= 1u;
-            if (!(ok = wait(&v_full[vst], vph))) break;
-            s_taken[1] = ++nv;
-            // V rows that no query sees (the tails of the last cached page and of
-            // the window) become zeros: 0 * NaN would reach every row
-            const int c_own = prev.own_keys - t * kSharedTile;  // cached keys of this tile
-            const int c_win = prev.n_own * kPageBlock - t * kSharedTile + A.W;  // window's end
-#pragma unroll 1
-            for (int part = 0; part < 2; ++part) {
-              const int c = part ? c_win : c_own;
-              if (prev.b < 0 || c <= 0 || c >= kSharedTile || !(c & 15)) continue;
-              const int rows = 16 - (c & 15);
-#pragma unroll 1
-              for (int e = lane; e < rows * (HD / 8); e += 32)
-                *reinterpret_cast<uint4*>(v_ring + vst * C::kTileBytes +
-                                          2 * ((c >> 4) * kPageBlock * HD +
-                                               tile_off((c & 15) + e % rows, e / rows * 8, HD))) =
-                    make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-            }
-            __syncwarp();
-          }
-          if (!(ok = wait(&p_full[x], x ? pph1 : pph0))) break;
-          if (x) pph1 ^= 1u; else pph0 ^= 1u;
-          if (elect_one()) {
-            tc_fence_after();
-            const uint64_t dv = dv0 + (uint64_t)(vst * C::kTileBytes >> 4);
-            const uint32_t d = tmem + kColO + (uint32_t)(x * 128);
-            const uint32_t p = tmem + kColS + (uint32_t)(x * 128);
-#pragma unroll
-            for (int k = 0; k < kSharedTilePages; ++k)  // 16 keys: 8 columns of P
-              if (k < np) mma_ts(d, p + k * 8, dv + k * (HD * 2), idPV, (pj || k) ? 1u : 0u);
-            tc_commit(&pv_done[x]);
-            if (x == 1 || !prev.pair) tc_commit(&v_empty[vst]);
-          }
-          __syncwarp();
-        }
-        if (have && (x == 0 || j < cur.nB)) {
-          const int t = seg_tile(cur, x, j), np = tile_pages(cur, t);
-          if (j == 0 && (cur.pair || x == 0)) {  // a new segment's Q
-            qbuf = cur.pair ? x : flip;
-            if (!cur.pair) flip ^= 1;
-            const int nq = qbuf ? nq1++ : nq0++;
-            if (!(ok = wait(&q_full[qbuf], (uint32_t)(nq & 1)))) break;
-            s_taken[2 + qbuf] = nq + 1;
-          }
-          if (x == 0 || !cur.pair) {
-            if (++kst == C::kK) kst = 0;
-            if (kst == 0) kph ^= 1u;
-            if (!(ok = wait(&k_full[kst], kph))) break;
-            s_taken[0] = ++nk;
-          }
-          const int buf = cur.pair ? x : qbuf;
-          if (elect_one()) {
-            tc_fence_after();
-            const uint64_t dq = dq0 + (uint64_t)(buf * C::kQBytes >> 4);
-            const uint64_t dk = dk0 + (uint64_t)(kst * C::kTileBytes >> 4);
-            const uint32_t id = idesc_bf16_m128(np * kPageBlock);
-            const uint32_t d = tmem + kColS + (uint32_t)(x * 128);
-#pragma unroll
-            for (int k = 0; k < HD / 16; ++k)  // 16 dims: two 8-dim groups
-              tc_mma_f16(d, dq + k * 256, dk + k * 16, id, k ? 1u : 0u);
-            tc_commit(&s_full[x]);
-            if (x == 1 || !cur.pair) tc_commit(&k_empty[kst]);
-            // the last S of the segment from this Q
-            if (cur.pair ? j + 1 == cur.n : t + 1 == cur.t1) tc_commit(&q_empty[buf]);
-          }
-          __syncwarp();
-        }
-      }
-      held = have;
-      prev = cur;
-      pj = j;
-      if (have && ++j == cur.n) {
+    while (true) {
+      // This stream's next tile, or none in this round: one segment on at most, for
+      // the planner publishes only a few ahead of the slowest reader, which may be
+      // waiting for the P V due here.
+      ++j;
+      if (have && j >= (x ? g.nB : g.n)) {
+        base_n += g.t1 - g.t0;
+        if (g.pair || !flip) ++nq0;
+        if (g.pair || flip) ++nq1;
+        if (!g.pair) flip ^= 1;
         j = 0;
-        have = get(cur);
+        have = get(g);
       }
+      if (!have && pn < 0) break;
+      const bool tile = have && j < (x ? g.nB : g.n);
+      const int buf = g.pair ? x : flip;
+      int t = 0, n = 0, np = 0, kst = 0;
+      if (tile) {
+        if (j == 0 && !(ok = wait(&q_full[buf], (uint32_t)((buf ? nq1 : nq0) & 1)))) break;
+        t = seg_tile(g, x, j);
+        np = tile_pages(g, t);
+        n = base_n + t - g.t0;
+        const int use = n / C::kK;
+        kst = n - use * C::kK;
+        if (!(ok = wait(&k_full[kst], (uint32_t)(use & 1)))) break;
+      }
+      int vst = 0;
+      if (pn >= 0) {
+        const int use = pn / C::kV;
+        vst = pn - use * C::kV;
+        if (!(ok = wait(&v_full[vst], (uint32_t)(use & 1)))) break;
+        // V rows that no query sees (the tails of the last cached page and of the
+        // window) become zeros: 0 * NaN would reach every row.  In pair mode both
+        // issuers write the same zeros.
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          const int c = part ? pc1 : pc0;
+          if (c <= 0 || c >= kSharedTile || !(c & 15)) continue;
+          const int rows = 16 - (c & 15);
+#pragma unroll 1
+          for (int e = lane; e < 16 * (HD / 8); e += 32)
+            if ((e & 15) < rows)
+              *reinterpret_cast<uint4*>(v_ring + vst * C::kTileBytes +
+                                        2 * ((c >> 4) * kPageBlock * HD +
+                                             tile_off((c & 15) + (e & 15), (e >> 4) * 8, HD))) =
+                  make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        if (!(ok = wait(&p_full[x], pph))) break;
+        pph ^= 1u;
+      }
+      if (elect_one()) {
+        tc_fence_after();
+        if (pn >= 0) {
+          const uint64_t dv = dv0 + (uint64_t)(vst * C::kTileBytes >> 4);
+#pragma unroll
+          for (int k = 0; k < kSharedTilePages; ++k)  // 16 keys: 8 columns of P
+            if (k < pnp) mma_ts(dO, dS + k * 8, dv + k * (HD * 2), idPV, (k || !pfirst) ? 1u : 0u);
+          tc_commit(&pv_done[x]);
+          tc_commit(&v_empty[vst]);
+          if (!ppair) tc_commit(&v_empty[vst]);
+        }
+        if (tile) {
+          const uint64_t dq = dq0 + (uint64_t)(buf * C::kQBytes >> 4);
+          const uint64_t dk = dk0 + (uint64_t)(kst * C::kTileBytes >> 4);
+          const uint32_t id = idesc_bf16_m128(np * kPageBlock);
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k)  // 16 dims: two 8-dim groups
+            tc_mma_f16(dS, dq + k * 256, dk + k * 16, id, k ? 1u : 0u);
+          tc_commit(&s_full[x]);
+          tc_commit(&k_empty[kst]);
+          if (!g.pair) tc_commit(&k_empty[kst]);
+          if (j + 1 == (x ? g.nB : g.n)) {  // this stream's last S from this Q
+            tc_commit(&q_empty[buf]);
+            if (g.pair || g.nB == 0) tc_commit(&q_empty[buf]);
+          }
+        }
+      }
+      __syncwarp();
+      pn = tile ? n : -1;
+      pnp = np;
+      pfirst = j == 0;
+      ppair = g.pair;
+      pc0 = g.b < 0 ? 0 : g.own_keys - t * kSharedTile;
+      pc1 = g.b < 0 ? 0 : g.n_own * kPageBlock - t * kSharedTile + A.W;
     }
     // every MMA has completed before TMEM is freed
     if (elect_one()) tc_commit(&fin);
@@ -591,11 +606,14 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             float e[16];
             uint32_t u[16];
             ld16(tS + c0, e);
+            // bit i: column c0 + i is visible
+            const uint32_t lo = c_own - c0 >= 16 ? ~0u : c_own <= c0 ? 0u : (1u << (c_own - c0)) - 1;
+            const uint32_t up = c_end - c0 >= 16 ? ~0u : c_end <= c0 ? 0u : (1u << (c_end - c0)) - 1;
+            const uint32_t dn = c_win - c0 >= 16 ? ~0u : c_win <= c0 ? 0u : (1u << (c_win - c0)) - 1;
+            const uint32_t seen = lo | (up & ~dn);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int c = c0 + i;
-              u[i] = c < c_own || (c >= c_win && c < c_end) ? __float_as_uint(e[i]) : 0xff800000u;
-            }
+            for (int i = 0; i < 16; ++i)
+              u[i] = seen >> i & 1 ? __float_as_uint(e[i]) : 0xff800000u;
             st16(tS + c0, u);
           }
           wait_st();
@@ -640,68 +658,66 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       const int urows = g.b < 0 ? A.srows : A.prows;
       float4* po = (g.b < 0 ? A.part_s : A.part_p) + (size_t)g.slot * urows * (HD / 4);
       float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + (size_t)g.slot * urows;
-      if (g.pair) {
-        const int row = x * TPB * G + r;
-#pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          float o[32];
-          ld32(tO + c, o);
-          if (valid)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              po[(size_t)(c / 4 + k) * urows + row] =
-                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        }
-        if (valid) ml[row] = make_float2(m, l);
-        tc_fence_before();
-      } else {
-        // join A and B: each warpgroup takes half of the dims of both
+      // pair: all dims of this stream's O.  split: A and B are joined, each
+      // warpgroup takes half of the dims of both.
+      const int row = (g.pair ? x * TPB * G : 0) + r;
+      float fa = 1.f, fb = 0.f, M = m, ls = l;
+      if (!g.pair) {
         s_ml[x][r] = make_float2(m, l);
         tc_fence_before();
         both();
         tc_fence_after();
         const float2 o_ml = s_ml[x ^ 1][r];
-        const float M = fmaxf(m, o_ml.x);
+        M = fmaxf(m, o_ml.x);
         const float am = m == -INFINITY ? 0.f : ex2_approx(m - M);
         const float ao = o_ml.x == -INFINITY ? 0.f : ex2_approx(o_ml.x - M);
-        const float fa = x ? ao : am, fb = x ? am : ao;  // factors of A's and B's O
-        const uint32_t t0 = tmem + lane_off + kColO + (uint32_t)(x * HD / 2);
-#pragma unroll 1
-        for (int c = 0; c < HD / 2; c += 32) {
-          float o[32];
-          ld32(t0 + c, o);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] *= fa;
-          if (g.nB > 0) {  // else B's O holds nothing of this segment
-            float ob[32];
-            ld32(t0 + 128 + c, ob);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = fmaf(ob[k], fb, o[k]);
-          }
-          if (valid)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              po[(size_t)((x * (HD / 2) + c) / 4 + k) * urows + r] =
-                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        }
-        if (valid && x == 0) ml[r] = make_float2(M, l * am + o_ml.y * ao);
-        tc_fence_before();
-        both();  // O and s_ml may be written again
+        fa = x ? ao : am;
+        fb = x ? am : ao;
+        ls = l * am + o_ml.y * ao;
       }
+      const int nd = g.pair ? HD : HD / 2, d0 = g.pair ? 0 : x * (HD / 2);
+      const uint32_t src = tmem + lane_off + kColO + (uint32_t)(g.pair ? x * 128 : d0);
+      float4* dst = po + (size_t)(d0 / 4) * urows + row;
+#pragma unroll 1
+      for (int c = 0; c < nd; c += 16) {
+        float o[16];
+        ld16(src + c, o);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] *= fa;
+        if (!g.pair && g.nB > 0) {  // else B's O holds nothing of this segment
+          float ob[16];
+          ld16(src + 128 + c, ob);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = fmaf(ob[k], fb, o[k]);
+        }
+        if (valid) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            *dst = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            dst += urows;
+          }
+        }
+      }
+      if (valid && (g.pair || x == 0)) ml[row] = make_float2(M, ls);
+      tc_fence_before();
+      if (!g.pair) both();  // O and s_ml may be written again
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (s_abort && threadIdx.x == 256) {
-    // a wait expired: let the copies still in flight land (bounded)
-    for (int i = s_taken[0]; i < s_issued[0]; ++i)
+    // a wait expired: let the copies still in flight land (bounded; a phase that
+    // has passed answers at once)
+#pragma unroll 1
+    for (int i = max(0, s_issued[0] - C::kK); i < s_issued[0]; ++i)
       mbar_wait(&k_full[i % C::kK], (uint32_t)(i / C::kK) & 1u, A.err);
-    for (int i = s_taken[1]; i < s_issued[1]; ++i)
+#pragma unroll 1
+    for (int i = max(0, s_issued[1] - C::kV); i < s_issued[1]; ++i)
       mbar_wait(&v_full[i % C::kV], (uint32_t)(i / C::kV) & 1u, A.err);
+#pragma unroll 1
     for (int x = 0; x < 2; ++x)
-      for (int i = s_taken[2 + x]; i < s_issued[2 + x]; ++i)
-        mbar_wait(&q_full[x], (uint32_t)i & 1u, A.err);
+      if (s_issued[2 + x]) mbar_wait(&q_full[x], (uint32_t)(s_issued[2 + x] - 1) & 1u, A.err);
   }
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);

@@ -48,16 +48,15 @@ struct SharedArgs {
 // cached length of sequence b as the kernels see it, and the pages of it that
 // come from the shared list (all of them or none)
 struct SeqSpan { int len, shared; };
-__device__ __forceinline__ SeqSpan seq_span(const SharedArgs& A, int b, bool tell) {
-  int L = A.seq_len[b];
-  if (L < 0) {
-    if (tell) set_err(A.err, WEDLM_DEV_BAD_SEQLEN);
-    L = 0;
-  } else if (L > A.max_pages * kPageBlock) {
-    if (tell) set_err(A.err, WEDLM_DEV_CAPACITY);
-    L = A.max_pages * kPageBlock;
-  }
+__device__ __forceinline__ SeqSpan seq_span(const SharedArgs& A, int b) {
+  const int L = max(0, min(A.seq_len[b], A.max_pages * kPageBlock));
   return {L, L >= A.nsp * kPageBlock ? A.nsp : 0};
+}
+// records a length that seq_span has to change
+__device__ __forceinline__ void check_len(const SharedArgs& A, int b) {
+  const int L = A.seq_len[b];
+  if (L < 0 || L > A.max_pages * kPageBlock)
+    set_err(A.err, L < 0 ? WEDLM_DEV_BAD_SEQLEN : WEDLM_DEV_CAPACITY);
 }
 __device__ __forceinline__ int own_pages(const SeqSpan& s) {
   return (s.len + kPageBlock - 1) / kPageBlock - s.shared;
@@ -81,103 +80,99 @@ struct SharedSeg {
 // the total below 2^31, so that the divisions are 32 bits wide: the planner runs
 // before the first copy can start.
 struct SharedWalk {
-  int u0, w0, w1;       // weighted start of the next unit, the block's share
+  int u0, w0, w1;        // weighted start of the next unit, the block's share
   int shared_tiles, u, b, k;  // next unit: shared unit u, or unit k of sequence b
+  int uw;                // weight of a unit of the range at hand
+  SeqSpan sp;
 
-  __device__ int unit_weight(const SharedArgs& A, const SeqSpan& sp) const {
-    return A.ucost + own_tiles(A, sp) * A.private_cost;
-  }
   __device__ void init(const SharedArgs& A) {
     const int lane = threadIdx.x & 31, units = A.nkv * A.pblocks;
     const int per = (A.B + 31) / 32, b0 = min(A.B, lane * per), b1 = min(A.B, b0 + per);
-    int sum = 0;
-    bool any = false;
+    int sum = 0, any = 0;
 #pragma unroll 1
     for (int i = b0; i < b1; ++i) {
-      const SeqSpan sp = seq_span(A, i, blockIdx.x == 0);
-      any |= sp.shared > 0;
-      sum += units * unit_weight(A, sp);
+      if (blockIdx.x == 0) check_len(A, i);
+      const SeqSpan s = seq_span(A, i);
+      any |= s.shared;
+      sum += units * (A.ucost + own_tiles(A, s) * A.private_cost);
     }
     any = __any_sync(0xffffffffu, any);
     int incl = sum;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
     // nothing to do for the shared pages when no sequence takes part
     shared_tiles = any ? (A.nsp + kSharedTilePages - 1) / kSharedTilePages : 0;
-    const int shared_unit = any ? A.ucost + shared_tiles * A.shared_cost : 0;
-    const int shared_total = shared_unit * A.nkv * A.sblocks;
+    uw = A.ucost + shared_tiles * A.shared_cost;
+    const int shared_total = any ? uw * A.nkv * A.sblocks : 0;
     const unsigned total = shared_total + __shfl_sync(0xffffffffu, incl, 31);
     // a share is never shorter than min_share >= a tile, so that it holds a
     // tile's start wherever it lies inside a unit
     const unsigned blocks = max(1u, min((unsigned)A.grid, total / (unsigned)A.min_share));
-    u = b = k = 0;
-    w0 = w1 = u0 = 0;
-    if (blockIdx.x >= blocks) {
-      b = A.B;
-      return;
-    }
     const unsigned share = total / blocks, extra = total - share * blocks;
     w0 = blockIdx.x * share + min(blockIdx.x, extra);
     w1 = w0 + share + (blockIdx.x < extra ? 1 : 0);
-    if (w0 < shared_total) {
-      u = (unsigned)w0 / (unsigned)shared_unit;
-      u0 = u * shared_unit;
-    } else {
+    u = b = k = u0 = 0;
+    if (blockIdx.x >= blocks) {
+      b = A.B;
       u = A.nkv * A.sblocks;
-      const int r = w0 - shared_total;
-      const int owner = __ffs(__ballot_sync(0xffffffffu, incl > r)) - 1;
-      int at = incl - sum, i = b0;
-      if (lane == owner) {
-#pragma unroll 1
-        for (; i + 1 < b1; ++i) {
-          const int w = units * unit_weight(A, seq_span(A, i, false));
-          if (r < at + w) break;
-          at += w;
-        }
-      }
-      b = __shfl_sync(0xffffffffu, i, owner);
-      at = __shfl_sync(0xffffffffu, at, owner);
-      const int uw = unit_weight(A, seq_span(A, b, false));
-      k = (unsigned)(r - at) / (unsigned)uw;
-      u0 = shared_total + at + k * uw;
+    } else if (w0 < shared_total) {
+      u = (unsigned)w0 / (unsigned)uw;
+      u0 = u * uw;
+    } else {  // the first sequence of the lane in whose range the share starts
+      u = A.nkv * A.sblocks;
+      const int owner = __ffs(__ballot_sync(0xffffffffu, incl > w0 - shared_total)) - 1;
+      b = owner * per;
+      u0 = shared_total + __shfl_sync(0xffffffffu, incl - sum, owner);
     }
   }
   __device__ bool next(const SharedArgs& A, SharedSeg& g) {
-    while (b < A.B && u0 < w1) {
-      int cost;
-      if (u < A.nkv * A.sblocks && shared_tiles) {
+#pragma unroll 1
+    while (true) {
+      int cost = A.shared_cost;
+      if (shared_tiles && u < A.nkv * A.sblocks) {
         g.unit = u;
         g.b = -1;
         g.kvh = u / A.sblocks;
         g.blk = u - g.kvh * A.sblocks;
         g.T = shared_tiles;
         g.sp = SeqSpan{0, 0};
-        cost = A.shared_cost;
+        if (u0 >= w1) return false;
         ++u;
       } else {
-        const int per = A.nkv * A.pblocks;
-        g.unit = A.nkv * A.sblocks + b * per + k;
-        g.b = b;
-        g.kvh = k / A.pblocks;
-        g.blk = k - g.kvh * A.pblocks;
-        g.sp = seq_span(A, b, false);
-        g.T = own_tiles(A, g.sp);
+        if (b >= A.B || u0 >= w1) return false;
+        const int units = A.nkv * A.pblocks;
+        if (k == 0) {  // a sequence's first unit: skip to where the share starts
+          sp = seq_span(A, b);
+          uw = A.ucost + own_tiles(A, sp) * A.private_cost;
+          if (u0 < w0) k = min(units, (w0 - u0) / uw);
+          u0 += k * uw;
+        }
+        const bool here = k < units;
+        if (here) {
+          g.unit = A.nkv * A.sblocks + b * units + k;
+          g.b = b;
+          g.kvh = k / A.pblocks;
+          g.blk = k - g.kvh * A.pblocks;
+          g.sp = sp;
+          g.T = own_tiles(A, sp);
+          ++k;
+        }
         cost = A.private_cost;
-        if (++k == per) {
+        if (k == units) {
           k = 0;
           ++b;
         }
+        if (!here) continue;  // the whole sequence lies before the share
       }
-      const int first = w0 - u0 - A.ucost, end = w1 - u0 - A.ucost, len = g.T * cost;
-      g.t0 = first <= 0 ? 0 : first >= len ? g.T : (first + cost - 1) / cost;
-      g.t1 = end <= 0 ? 0 : end >= len ? g.T : (end + cost - 1) / cost;
-      u0 += A.ucost + len;
+      const int start = u0 + A.ucost;
+      u0 = start + g.T * cost;
+      g.t0 = w0 <= start ? 0 : min(g.T, (w0 - start + cost - 1) / cost);
+      g.t1 = w1 <= start ? 0 : min(g.T, (w1 - start + cost - 1) / cost);
       if (g.t0 < g.t1) return true;
     }
-    return false;
   }
 };
 

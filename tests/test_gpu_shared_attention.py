@@ -66,6 +66,14 @@ def test_many_row_blocks_and_long_ranges(dtype):
     c.check(c.call())
 
 
+@pytest.mark.parametrize("B,own", [(300, 5), (500, 0), (200, 130)])
+def test_many_short_private_units_behind_shared_ones(B, own):
+    """Blocks that go from long shared segments to a run of one- and two-tile
+    private ones."""
+    c = AttnCase([16 * 40 + own] * B, 1, 8, 2, 128, 40, BF, seed=B)
+    c.check(c.call())
+
+
 def test_batch_of_1024_single_tokens():
     c = AttnCase([16 * 4 + (b % 40) for b in range(1024)], 1, 4, 1, 64, 4, BF, seed=7)
     c.check(c.call())
