@@ -36,11 +36,12 @@
 // a tile is unrolled.
 //
 // Warps (384 threads): 0-3 softmax of A (thread = row), 4-7 of B, 8 copies Q (TMA
-// boxes), K and V (4 KiB bulk copies of whole pages, already in the 8x8-tile
-// operand layout), 9 and 11 issue the MMAs of A and B, 10 plans: it walks the
-// split and publishes the segments ahead of their use.  A row's 128 scores are
-// taken in two halves of 64, the second one read from TMEM twice, so that the
-// softmax fits the 168 registers a thread has.
+// boxes) and K, 10 copies V (4 KiB bulk copies of whole pages, already in the
+// 8x8-tile operand layout; one warp for both took 1,900 cycles a tile where the
+// MMAs take 1,024) and plans: it walks the split and publishes the segments ahead
+// of their use; 9 and 11 issue the MMAs of A and B.  A row's 128 scores are taken
+// in two halves of 64, the second one read from TMEM twice, so that the softmax
+// fits the 168 registers a thread has.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -252,8 +253,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   __shared__ Seg s_seg[kSegs];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_issued[4];  // copies of K, V, Q buffer 0 and 1 started
-  __shared__ const bf16* s_src[kSharedTilePages];
-  __shared__ int s_ids[4][kSharedTilePages];  // page ids of K tiles whose V is to come
+  __shared__ __align__(16) const bf16* s_src[2][kSharedTilePages];
   __shared__ float2 s_ml[2][128];
 
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 127) &
@@ -281,7 +281,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 11);  // copier, issuers, 8 softmax warps
+      mbar_init(&seg_empty[i], 12);  // copiers, issuers, 8 softmax warps
       s_issued[i] = 0;
     }
     mbar_init(&joined, 8);
@@ -304,8 +304,8 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     return __all_sync(0xffffffffu, ok);
   };
   // next published segment, into registers (warp-wide); false after the last
-  int seg_i = 0;
-  uint32_t seg_ph = 0;
+  int seg_i = 0, pub_i = 0;
+  uint32_t seg_ph = 0, pub_ph = 0;
   auto get = [&](Seg& g) -> bool {
     if (!wait(&seg_full[seg_i], seg_ph)) return false;
     g = s_seg[seg_i];
@@ -320,15 +320,21 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 
   pdl_wait();  // nothing of an earlier kernel is read before
   pdl_trigger();
-  if (warp == 10) {
-    // ---------------- planner ----------------
+  if (warp == 8 || warp == 10) {
+    // ---------------- copiers: Q and K (8), V (10); 10 plans too ----------------
+    const int kv = warp == 10;
+    uint64_t* full = kv ? v_full : k_full;
+    uint64_t* empty = kv ? v_empty : k_empty;
+    uint8_t* ring = kv ? v_ring : k_ring;
+    const int NS = kv ? C::kV : C::kK;
+    const uint64_t keep = l2_evict_last_policy(), once = l2_evict_first_policy();
     SharedWalk walk;
-    walk.init(A);
-    SharedSeg u;
-    bool more;
-#pragma unroll 1
-    do {
-      more = __shfl_sync(0xffffffffu, walk.next(A, u), 0);
+    bool planned = true;  // the whole list is published
+    // publish the next segment of the block's share, or the end of the list; this
+    // warp keeps one segment ahead of the one it copies
+    auto publish = [&]() -> bool {
+      SharedSeg u;
+      const bool more = __shfl_sync(0xffffffffu, walk.next(A, u), 0);
       Seg g = {};
       if (more) {
         const int n = u.t1 - u.t0;
@@ -353,71 +359,72 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         g.n = g.pair ? n : (n + 1) / 2;
         g.nB = g.pair ? n : n / 2;
         g.slot = seg_slot(A, u.unit, blockIdx.x);
-        if (lane == 0) record_unit(A, u);
       }
-      if (!wait(&seg_empty[seg_i], seg_ph ^ 1u)) break;
+      planned = !more;
+      if (!wait(&seg_empty[pub_i], pub_ph ^ 1u)) return false;
       if (lane == 0) {
-        s_seg[seg_i] = g;
-        mbar_arrive(&seg_full[seg_i]);
+        s_seg[pub_i] = g;
+        mbar_arrive(&seg_full[pub_i]);
+        if (more) record_unit(A, u);
       }
       __syncwarp();
-      if (++seg_i == kSegs) {
-        seg_i = 0;
-        seg_ph ^= 1u;
+      if (++pub_i == kSegs) {
+        pub_i = 0;
+        pub_ph ^= 1u;
       }
-    } while (more);
-  } else if (warp == 8) {
-    // ---------------- copier ----------------
-    const uint64_t keep = l2_evict_last_policy(), once = l2_evict_first_policy();
-    if (elect_one()) tma_prefetch_desc(&mq);
-    int nk = 0, nv = 0, nq0 = 0, nq1 = 0, flip = 0;
-    // this lane's page id of a K tile, loaded a tile ahead of its use
+      return true;
+    };
+    if (kv) {
+      walk.init(A);
+      planned = false;
+    } else if (elect_one()) {
+      tma_prefetch_desc(&mq);
+    }
+    int st = 0, issued = 0, nq0 = 0, nq1 = 0, flip = 0;
+    uint32_t ph = 1;
+    // this lane's page id of a tile, loaded a tile ahead of its use
     auto id_of = [&](const Seg& g, int t) -> int {
       const int j = t * kSharedTilePages + lane;
       return lane < kSharedTilePages && t < g.t1 && j < (g.b < 0 ? g.pages : g.n_own)
                  ? own_page_id(A, g.b, g.shared, j)
                  : -1;
     };
-    Seg g;
-    bool ok = get(g);
-    int next_id = ok ? id_of(g, g.t0) : -1;
+    Seg g, nxt;
+    int next_id = -1;
+    bool ok = true, more = false;
 #pragma unroll 1
-    while (ok) {
-      // Q: A's and B's row block, or one buffer in turn for both
+    for (bool first = true; ok; first = false) {
+      if (!planned && !(ok = publish())) break;
+      if (!first) {
+        // Q: A's and B's row block, or one buffer in turn for both
 #pragma unroll 1
-      for (int x = 0; x < 1 + g.pair; ++x) {
-        const int buf = g.pair ? x : flip;
-        const int nq = buf ? nq1++ : nq0++;
-        if (!(ok = wait(&q_empty[buf], (uint32_t)(nq & 1) ^ 1u))) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&q_full[buf], (uint32_t)(min(TPB, A.B * A.W) * G) * HD * 2);
+        for (int x = 0; !kv && x < 1 + g.pair; ++x) {
+          const int buf = g.pair ? x : flip;
+          const int nq = buf ? nq1++ : nq0++;
+          if (!(ok = wait(&q_empty[buf], (uint32_t)(nq & 1) ^ 1u))) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&q_full[buf], (uint32_t)(min(TPB, A.B * A.W) * G) * HD * 2);
 #pragma unroll 1
-          for (int c = 0; c < HD / 8; ++c)
-            load_q_box(base + buf * C::kQBytes + c * 2048, &mq, &q_full[buf], 8 * c, g.kvh * G,
-                       g.tok0 + x * TPB);
-          s_issued[2 + buf] = nq + 1;
+            for (int c = 0; c < HD / 8; ++c)
+              load_q_box(base + buf * C::kQBytes + c * 2048, &mq, &q_full[buf], 8 * c, g.kvh * G,
+                         g.tok0 + x * TPB);
+            s_issued[2 + buf] = nq + 1;
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!g.pair) flip ^= 1;
       }
-      if (!g.pair) flip ^= 1;
-      Seg nxt;
-      const bool more = ok && get(nxt);
-      // K0, K1, V0, K2, V1, .. , V of the last
-      const int T = g.t1 - g.t0;
+      more = ok && get(nxt);
+      if (first) {
+        if (!more) break;
+        g = nxt;
+        next_id = id_of(g, g.t0);
+        continue;
+      }
 #pragma unroll 1
-      for (int i = 0; ok && i < 2 * T; ++i) {
-        const int m = (i + 1) >> 1;
-        const int kv = i > 0 && (!(i & 1) || m == T);
-        const int t = g.t0 + (!kv ? m : i & 1 ? T - 1 : (i >> 1) - 1);
-        const int np = tile_pages(g, t), j = t * kSharedTilePages + lane;
-        int id = next_id;
-        const int n = kv ? nv++ : nk++;
-        if (kv) {
-          id = s_ids[n & 3][lane & 7];  // V follows in K's order, at most 3 behind
-        } else {
-          if (lane < kSharedTilePages) s_ids[n & 3][lane] = id;
-          next_id = t + 1 < g.t1 ? id_of(g, t + 1) : more ? id_of(nxt, nxt.t0) : -1;
-        }
+      for (int t = g.t0; ok && t < g.t1; ++t) {
+        const int np = tile_pages(g, t), j = t * kSharedTilePages + lane, id = next_id;
+        next_id = t + 1 < g.t1 ? id_of(g, t + 1) : more ? id_of(nxt, nxt.t0) : -1;
         const bf16* src = nullptr;
         if (lane < np) {
           if (g.b >= 0 && j >= g.n_own)
@@ -427,29 +434,41 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           else
             set_err(A.err, WEDLM_DEV_BAD_PAGE);
         }
+        if (lane < kSharedTilePages) s_src[kv][lane] = src;
         const unsigned have = __ballot_sync(0xffffffffu, src != nullptr);
-        if (lane < kSharedTilePages) s_src[lane] = src;
-        const int NS = kv ? C::kV : C::kK, use = n / NS, st = n - use * NS;
-        uint64_t* full = (kv ? v_full : k_full) + st;
-        if (!(ok = wait((kv ? v_empty : k_empty) + st, (uint32_t)(use & 1) ^ 1u))) break;
-        uint8_t* dst = (kv ? v_ring : k_ring) + st * C::kTileBytes;
+        if (!(ok = wait(&empty[st], ph))) break;
+        uint8_t* dst = ring + st * C::kTileBytes;
+        uint64_t* bar = &full[st];
         if (__popc(have) < np) {  // page ids out of range read as zeros
 #pragma unroll 1
           for (int e = lane; e < np * (int)C::kPage / 16; e += 32)
             if (!(have >> (e / (C::kPage / 16)) & 1))
               reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (elect_one()) {
-          mbar_arrive_expect_tx(full, (uint32_t)__popc(have) * C::kPage);
-          const uint64_t pol = g.b < 0 ? keep : once;
-#pragma unroll
-          for (int p = 0; p < kSharedTilePages; ++p)
-            if (have >> p & 1) bulk_load(dst + p * C::kPage, s_src[p], C::kPage, full, pol);
-          s_issued[kv] = n + 1;
         }
         __syncwarp();
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, (uint32_t)__popc(have) * C::kPage);
+          const uint64_t pol = g.b < 0 ? keep : once;
+          if (have == (1u << kSharedTilePages) - 1) {
+            const bf16* sp[kSharedTilePages];
+#pragma unroll
+            for (int p = 0; p < kSharedTilePages; ++p) sp[p] = s_src[kv][p];
+#pragma unroll
+            for (int p = 0; p < kSharedTilePages; ++p)
+              bulk_load(dst + p * C::kPage, sp[p], C::kPage, bar, pol);
+          } else {
+#pragma unroll 1
+            for (int p = 0; p < kSharedTilePages; ++p)
+              if (have >> p & 1) bulk_load(dst + p * C::kPage, s_src[kv][p], C::kPage, bar, pol);
+          }
+          s_issued[kv] = ++issued;
+        }
+        __syncwarp();
+        if (++st == NS) {
+          st = 0;
+          ph ^= 1u;
+        }
       }
       if (!more) break;
       g = nxt;
