@@ -1,7 +1,7 @@
 // Shared-prefix window attention on the 5th-generation tensor cores (bf16).
 //
 // A block (one per SM) holds two streams, A and B: 128 query rows each of Q, S,
-// P and O, one warpgroup of softmax each.  A unit (a range of query rows of one
+// P and O.  A unit (a range of query rows of one
 // kv head, see shared_attn.cuh) takes them in one of two ways:
 //   pair:  more than one row block (TPB = 128/G tokens, at most 128 rows): A
 //          takes the first, B the second, and both read every K/V tile, so a
@@ -35,13 +35,12 @@
 // flat loop with its MMAs, copies and waits written once, and only the softmax of
 // a tile is unrolled.
 //
-// Warps (384 threads): 0-3 softmax of A (thread = row), 4-7 of B, 8 copies Q (TMA
-// boxes) and K, 10 copies V (4 KiB bulk copies of whole pages, already in the
-// 8x8-tile operand layout; one warp for both took 1,900 cycles a tile where the
-// MMAs take 1,024) and plans: it walks the split and publishes the segments ahead
-// of their use; 9 and 11 issue the MMAs of A and B.  A row's 128 scores are taken
-// in two halves of 64, the second one read from TMEM twice, so that the softmax
-// fits the 168 registers a thread has.
+// Warps (384 threads): 0-7 softmax, A's and B's tiles in turn, half of a tile's
+// keys each (a warpgroup per stream took 1,400 cycles from S to P, which the other
+// stream's 1,024 cycles of MMA did not cover); 8 copies Q (TMA boxes) and K, 10
+// copies V (4 KiB bulk copies of whole pages, already in the 8x8-tile operand
+// layout; one warp for both took 1,900 cycles a tile) and plans: it walks the split
+// and publishes the segments ahead of their use; 9 and 11 issue the MMAs of A and B.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -249,12 +248,13 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV];
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
-  __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], joined, fin;
+  __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], joined[4], fin;
   __shared__ Seg s_seg[kSegs];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_issued[4];  // copies of K, V, Q buffer 0 and 1 started
   __shared__ __align__(16) const bf16* s_src[2][kSharedTilePages];
-  __shared__ float2 s_ml[2][128];
+  __shared__ float s_red[2][2][128];  // [half][row]: row max of a tile; at the end, row sums
+  __shared__ int s_raise[2][4];                       // last tile that raised a maximum
 
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 127) &
                                              ~static_cast<uintptr_t>(127));
@@ -276,15 +276,15 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       mbar_init(&q_full[x], 1);
       mbar_init(&q_empty[x], 2);
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
+      mbar_init(&p_full[x], 8);
       mbar_init(&pv_done[x], 1);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_empty[i], 12);  // copiers, issuers, 8 softmax warps
-      s_issued[i] = 0;
+      mbar_init(&joined[i], 2);
+      s_issued[i] = s_raise[0][i] = s_raise[1][i] = 0;
     }
-    mbar_init(&joined, 8);
     mbar_init(&fin, 2);
     s_abort = 0;
     mbar_fence_init();
@@ -584,44 +584,47 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     mbar_wait(&fin, 0, A.err);
   } else {
     // ---------------- softmax ----------------
-    const int x = warp >> 2;                       // stream
-    const int r = threadIdx.x & 127;               // row of the stream's row block
-    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t tS = tmem + lane_off + kColS + (uint32_t)(x * 128);
-    const uint32_t tO = tmem + lane_off + kColO + (uint32_t)(x * 128);
+    // Warps q and q+4 hold query rows 32q .. 32q+31 of both streams (thread = row):
+    // q the keys 0-63 of a tile and the first half of O's dims, q+4 the others.
+    const int q = warp & 3, h = warp >> 2;
+    const int r = 32 * q + lane;
+    const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
     const float sc = A.scale_log2;
-    uint32_t sph = 0, dph = 0;  // phases of s_full and of pv_done
-    // both streams' warps meet; an mbarrier and not a named one, so that a wait
-    // that expired elsewhere cannot leave one side here for good
-    uint32_t jph = 0;
-    auto both = [&]() {
+    uint32_t sph = 0, dph = 0, jph = 0;  // phases: bit x of s_full and pv_done, of the pair's
+    // The two warps of a row meet.  An mbarrier and not a named one, so that a wait
+    // that expired elsewhere cannot leave one of them here for good.
+    auto pair_sync = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&joined);
-      wait(&joined, jph);
+      if (lane == 0) mbar_arrive(&joined[q]);
+      wait(&joined[q], jph);
       jph ^= 1u;
     };
     Seg g;
+    int tiles = 0;  // tiles so far, for the raise flags
+#pragma unroll 1
     while (get(g)) {
-      const int nx = x ? g.nB : g.n;
-      // token of this row within the unit, its window row
-      const int utok = (g.pair ? x * TPB : 0) + r / G;
-      const int p_row = g.w0 + utok;
-      const bool valid = r < TPB * G && utok < g.ntok;
-      float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < nx; ++j) {
+      float m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};
+#pragma unroll 1
+      for (int i = 0; i < g.n + g.nB; ++i) {
+        // A and B in turn (B's last tile may be missing)
+        const int x = i & 1, j = i >> 1;
         const int t = seg_tile(g, x, j), np = tile_pages(g, t);
-        wait(&s_full[x], sph);
-        sph ^= 1u;
+        const uint32_t tS = tl + kColS + (uint32_t)(x * 128);
+        const uint32_t tO = tl + kColO + (uint32_t)(x * 128 + h * (HD / 2));
+        float m = x ? m2[1] : m2[0];
+        wait(&s_full[x], sph >> x & 1);
+        sph ^= 1u << x;
         tc_fence_after();
         // what this row does not see becomes -inf, in TMEM and in a rolled loop:
         // only a unit's last tiles need it
         if (np < kSharedTilePages || (g.b >= 0 && (t + 1) * kSharedTile > g.own_keys)) {
+          const int p_row = g.w0 + (g.pair ? x * TPB : 0) + r / G;  // window row
           const int c_own = g.b < 0 ? np * kPageBlock : g.own_keys - t * kSharedTile;
           const int c_win = g.n_own * kPageBlock - t * kSharedTile;
           const int c_end = g.b < 0 ? 0 : c_win + p_row + 1;  // window keys up to this row
 #pragma unroll 1
-          for (int c0 = 0; c0 < kSharedTile; c0 += 16) {
-            if (c0 + 16 <= c_own) continue;  // the same for the warpgroup
+          for (int c0 = h * 64; c0 < h * 64 + 64; c0 += 16) {
+            if (c0 + 16 <= c_own) continue;  // the same for every row
             float e[16];
             uint32_t u[16];
             ld16(tS + c0, e);
@@ -631,25 +634,30 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             const uint32_t dn = c_win - c0 >= 16 ? ~0u : c_win <= c0 ? 0u : (1u << (c_win - c0)) - 1;
             const uint32_t seen = lo | (up & ~dn);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              u[i] = seen >> i & 1 ? __float_as_uint(e[i]) : 0xff800000u;
+            for (int k = 0; k < 16; ++k)
+              u[k] = seen >> k & 1 ? __float_as_uint(e[k]) : 0xff800000u;
             st16(tS + c0, u);
           }
           wait_st();
         }
         float v[64];
-        ld64(tS + 64, v);
-        const float mx1 = max64(v);
-        ld64(tS, v);
-        const float mt = fmaxf(mx1, max64(v)) * sc;
-        const bool raise = mt > m + kRaise;
-        if (__any_sync(0xffffffffu, raise)) {  // TMEM accesses are warp-wide
+        ld64(tS + h * 64, v);
+        float mt = max64(v) * sc;
+        // Does a row of either warp raise its maximum?  The meeting also keeps P
+        // from S columns the other warp has not read yet.
+        const int odd = ++tiles & 1;  // one of the two may be a tile ahead: two sets
+        s_red[odd][h][r] = mt;
+        if (__any_sync(0xffffffffu, mt > m + kRaise)) s_raise[odd][q] = tiles;
+        pair_sync();
+        if (s_raise[odd][q] == tiles) {
+          mt = fmaxf(mt, s_red[odd][h ^ 1][r]);
+          const bool raise = mt > m + kRaise;
           if (j > 0) {
             const float a = !raise ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - mt);
-            wait(&pv_done[x], dph ^ 1u);  // P V of the tile before is in O
+            wait(&pv_done[x], (dph >> x & 1) ^ 1u);  // P V of the tile before is in O
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < HD; c += 16) {
+            for (int c = 0; c < HD / 2; c += 16) {
               float o[16];
               uint32_t u[16];
               ld16(tO + c, o);
@@ -657,69 +665,72 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
               for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * a);
               st16(tO + c, u);
             }
-            l *= a;
+            if (x) l2[1] *= a; else l2[0] *= a;
           }
           if (raise) m = mt;
+          if (x) m2[1] = m; else m2[0] = m;
         }
-        const float nm = m == -INFINITY ? 0.f : -m;
-        l += exp64(tS, v, sc, nm);  // P over the columns just read
-        ld64(tS + 64, v);
-        l += exp64(tS + 32, v, sc, nm);
+        const float ps = exp64(tS + h * 32, v, sc, m == -INFINITY ? 0.f : -m);
+        if (x) l2[1] += ps; else l2[0] += ps;
         wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
-        dph ^= 1u;
+        dph ^= 1u << x;
       }
-      // the segment's partial: O once its last P V is done
-      if (nx > 0) wait(&pv_done[x], dph ^ 1u);
+      // The segment's partial: O once its last P V is done.  Pair: this warp's half
+      // of the dims of both streams' rows.  Split: A and B joined.
+      wait(&pv_done[0], (dph & 1) ^ 1u);
+      if (g.nB > 0) wait(&pv_done[1], (dph >> 1) ^ 1u);
       tc_fence_after();
+      pair_sync();  // the other warp is done with s_red too
+      s_red[h][0][r] = l2[0];  // the row sums are in halves
+      s_red[h][1][r] = l2[1];
+      pair_sync();
       const int urows = g.b < 0 ? A.srows : A.prows;
-      float4* po = (g.b < 0 ? A.part_s : A.part_p) + (size_t)g.slot * urows * (HD / 4);
+      float4* po = (g.b < 0 ? A.part_s : A.part_p) +
+                   ((size_t)g.slot * (HD / 4) + h * (HD / 8)) * urows;
       float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + (size_t)g.slot * urows;
-      // pair: all dims of this stream's O.  split: A and B are joined, each
-      // warpgroup takes half of the dims of both.
-      const int row = (g.pair ? x * TPB * G : 0) + r;
-      float fa = 1.f, fb = 0.f, M = m, ls = l;
+      float f[2] = {1.f, 1.f};
+      const float la = l2[0] + s_red[h ^ 1][0][r], lb = l2[1] + s_red[h ^ 1][1][r];
       if (!g.pair) {
-        s_ml[x][r] = make_float2(m, l);
-        tc_fence_before();
-        both();
-        tc_fence_after();
-        const float2 o_ml = s_ml[x ^ 1][r];
-        M = fmaxf(m, o_ml.x);
-        const float am = m == -INFINITY ? 0.f : ex2_approx(m - M);
-        const float ao = o_ml.x == -INFINITY ? 0.f : ex2_approx(o_ml.x - M);
-        fa = x ? ao : am;
-        fb = x ? am : ao;
-        ls = l * am + o_ml.y * ao;
+        const float M = fmaxf(m2[0], m2[1]);
+        f[0] = m2[0] == -INFINITY ? 0.f : ex2_approx(m2[0] - M);
+        f[1] = m2[1] == -INFINITY ? 0.f : ex2_approx(m2[1] - M);
+        if (h == 0 && r < g.ntok * G) ml[r] = make_float2(M, la * f[0] + lb * f[1]);
       }
-      const int nd = g.pair ? HD : HD / 2, d0 = g.pair ? 0 : x * (HD / 2);
-      const uint32_t src = tmem + lane_off + kColO + (uint32_t)(g.pair ? x * 128 : d0);
-      float4* dst = po + (size_t)(d0 / 4) * urows + row;
 #pragma unroll 1
-      for (int c = 0; c < nd; c += 16) {
-        float o[16];
-        ld16(src + c, o);
+      for (int x = 0; x < 1 + g.pair; ++x) {
+        const int row = x * TPB * G + r;
+        const bool valid = r < TPB * G && row < g.ntok * G;
+        if (g.pair && h == 0 && valid) ml[row] = make_float2(x ? m2[1] : m2[0], x ? lb : la);
+        const uint32_t tO = tl + kColO + (uint32_t)(x * 128 + h * (HD / 2));
+        float4* dst = po + row;
+#pragma unroll 1
+        for (int c = 0; c < HD / 2; c += 16) {
+          float o[16];
+          ld16(tO + c, o);
+          if (!g.pair) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] *= fa;
-        if (!g.pair && g.nB > 0) {  // else B's O holds nothing of this segment
-          float ob[16];
-          ld16(src + 128 + c, ob);
+            for (int k = 0; k < 16; ++k) o[k] *= f[0];
+            if (g.nB > 0) {  // else B's O holds nothing of this segment
+              float ob[16];
+              ld16(tO + 128 + c, ob);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = fmaf(ob[k], fb, o[k]);
-        }
-        if (valid) {
+              for (int k = 0; k < 16; ++k) o[k] = fmaf(ob[k], f[1], o[k]);
+            }
+          }
+          if (valid) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            *dst = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            dst += urows;
+            for (int k = 0; k < 4; ++k) {
+              *dst = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              dst += urows;
+            }
           }
         }
       }
-      if (valid && (g.pair || x == 0)) ml[row] = make_float2(M, ls);
       tc_fence_before();
-      if (!g.pair) both();  // O and s_ml may be written again
+      pair_sync();  // s_red may be written again
     }
   }
   tc_fence_before();
