@@ -381,7 +381,7 @@ typedef struct wedlm_append_args {
   int32_t batch;               /* B >= 1                                   */
   int32_t rows;                /* n >= 1 rows per sequence; <= 64 with
                                   kv_win; B*n < 2^31                       */
-  int32_t n_q_heads;           /* ignored without q                        */
+  int32_t n_q_heads;           /* ignored without q; heads 1..8192         */
   int32_t n_kv_heads, head_dim;/* head_dim 64 or 128                       */
   int32_t dtype;               /* WEDLM_BF16 | WEDLM_FP32                  */
   int32_t max_pages_per_seq;   /* columns of page_table                    */

@@ -44,10 +44,14 @@ bool shared_plan(const wedlm_shared_attn_args& a, SharedPlan* P) {
   A.sblocks = (rows + A.srows - 1) / A.srows;
   A.pblocks = (seq_rows + A.prows - 1) / A.prows;
   if (a.dtype == WEDLM_BF16) {
-    A.ucost = 3;
-    A.shared_cost = A.B * A.W > P->TPB ? 5 : 4;
-    A.private_cost = A.W > P->TPB ? 5 : 4;
-    A.min_share = 8;
+    // relative times, swept on GB300: a tile for 128 rows 16, for a pair of row
+    // blocks 20; a unit's start and end 24, more with the rows whose partial it
+    // writes.  (All tiles alike, ends 12: 579 us for 64 sequences x 32 rows over
+    // 16384 shared positions, 405 us with these.)
+    A.ucost = 24 + std::min(A.prows, 128) / 8;
+    A.shared_cost = A.B * A.W > P->TPB ? 20 : 16;
+    A.private_cost = A.W > P->TPB ? 20 : 16;
+    A.min_share = 32;
   } else {
     A.ucost = 1;
     A.shared_cost = A.private_cost = A.min_share = 1;
