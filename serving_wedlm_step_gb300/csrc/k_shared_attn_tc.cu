@@ -266,7 +266,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   if (threadIdx.x == 32) {
     for (int i = 0; i < C::kK; ++i) {
       mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 2);  // both issuers, or one of them twice
+      mbar_init(&k_empty[i], 2);  // both issuers
     }
     for (int i = 0; i < C::kV; ++i) {
       mbar_init(&v_full[i], 1);
@@ -389,42 +389,37 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                  ? own_page_id(A, g.b, g.shared, j)
                  : -1;
     };
-    Seg g, nxt;
-    int next_id = -1;
-    bool ok = true, more = false;
+    Seg g;
+    bool ok = true;
 #pragma unroll 1
     for (bool first = true; ok; first = false) {
       if (!planned && !(ok = publish())) break;
-      if (!first) {
-        // Q: A's and B's row block, or one buffer in turn for both
-#pragma unroll 1
-        for (int x = 0; !kv && x < 1 + g.pair; ++x) {
-          const int buf = g.pair ? x : flip;
-          const int nq = buf ? nq1++ : nq0++;
-          if (!(ok = wait(&q_empty[buf], (uint32_t)(nq & 1) ^ 1u))) break;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(&q_full[buf], (uint32_t)(min(TPB, A.B * A.W) * G) * HD * 2);
-#pragma unroll 1
-            for (int c = 0; c < HD / 8; ++c)
-              load_q_box(base + buf * C::kQBytes + c * 2048, &mq, &q_full[buf], 8 * c, g.kvh * G,
-                         g.tok0 + x * TPB);
-            s_issued[2 + buf] = nq + 1;
-          }
-          __syncwarp();
-        }
-        if (!g.pair) flip ^= 1;
-      }
-      more = ok && get(nxt);
       if (first) {
-        if (!more) break;
-        g = nxt;
-        next_id = id_of(g, g.t0);
+        if (!get(g)) break;
         continue;
       }
+      // Q: A's and B's row block, or one buffer in turn for both
+#pragma unroll 1
+      for (int x = 0; !kv && x < 1 + g.pair; ++x) {
+        const int buf = g.pair ? x : flip;
+        const int nq = buf ? nq1++ : nq0++;
+        if (!(ok = wait(&q_empty[buf], (uint32_t)(nq & 1) ^ 1u))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&q_full[buf], (uint32_t)(min(TPB, A.B * A.W) * G) * HD * 2);
+#pragma unroll 1
+          for (int c = 0; c < HD / 8; ++c)
+            load_q_box(base + buf * C::kQBytes + c * 2048, &mq, &q_full[buf], 8 * c, g.kvh * G,
+                       g.tok0 + x * TPB);
+          s_issued[2 + buf] = nq + 1;
+        }
+        __syncwarp();
+      }
+      if (!g.pair) flip ^= 1;
+      int next_id = ok ? id_of(g, g.t0) : -1;
 #pragma unroll 1
       for (int t = g.t0; ok && t < g.t1; ++t) {
         const int np = tile_pages(g, t), j = t * kSharedTilePages + lane, id = next_id;
-        next_id = t + 1 < g.t1 ? id_of(g, t + 1) : more ? id_of(nxt, nxt.t0) : -1;
+        next_id = id_of(g, t + 1);
         const bf16* src = nullptr;
         if (lane < np) {
           if (g.b >= 0 && j >= g.n_own)
@@ -470,8 +465,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           ph ^= 1u;
         }
       }
-      if (!more) break;
-      g = nxt;
+      if (!ok || !get(g)) break;
     }
   } else if (warp == 9 || warp == 11) {
     // ---------------- MMA issuers ----------------
@@ -487,9 +481,30 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     int j = -1;             // tile of this stream in the segment
     int base_n = 0;         // tiles of the block before the segment
     int nq0 = 0, nq1 = 0, flip = 0;
+    // Both issuers follow every K and V tile and every Q of the block in order,
+    // and release what the other one uses as soon as it is there: a barrier's
+    // parity tells two neighbouring phases apart, so a reader may not skip any.
+    int kpos = 0, vpos = 0, kst = 0, vst = 0;
+    uint32_t kph = 0, vph = 0;
+    auto wait_k = [&]() { return wait(&k_full[kst], kph); };
+    auto wait_v = [&]() { return wait(&v_full[vst], vph); };
+    auto next_k = [&]() {
+      ++kpos;
+      if (++kst == C::kK) {
+        kst = 0;
+        kph ^= 1u;
+      }
+    };
+    auto next_v = [&]() {
+      ++vpos;
+      if (++vst == C::kV) {
+        vst = 0;
+        vph ^= 1u;
+      }
+    };
     // the tile whose P V is due: its number, pages, whether O starts with it, the
     // ends of its cached keys and of the window in it
-    int pn = -1, pnp = 0, pfirst = 0, pc0 = 0, pc1 = 0, ppair = 0;
+    int pn = -1, pnp = 0, pfirst = 0, pc0 = 0, pc1 = 0;
     uint32_t pph = 0;
     bool have = get(g), ok = true;
 #pragma unroll 1
@@ -498,7 +513,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       // the planner publishes only a few ahead of the slowest reader, which may be
       // waiting for the P V due here.
       ++j;
-      if (have && j >= (x ? g.nB : g.n)) {
+      if (have && j >= max(1, x ? g.nB : g.n)) {
         base_n += g.t1 - g.t0;
         if (g.pair || !flip) ++nq0;
         if (g.pair || flip) ++nq1;
@@ -509,21 +524,33 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       if (!have && pn < 0) break;
       const bool tile = have && j < (x ? g.nB : g.n);
       const int buf = g.pair ? x : flip;
-      int t = 0, n = 0, np = 0, kst = 0;
-      if (tile) {
-        if (j == 0 && !(ok = wait(&q_full[buf], (uint32_t)((buf ? nq1 : nq0) & 1)))) break;
-        t = seg_tile(g, x, j);
-        np = tile_pages(g, t);
-        n = base_n + t - g.t0;
-        const int use = n / C::kK;
-        kst = n - use * C::kK;
-        if (!(ok = wait(&k_full[kst], (uint32_t)(use & 1)))) break;
+      if (have && j == 0) {  // a new segment's Q
+        if (!(ok = wait(&q_full[buf], (uint32_t)((buf ? nq1 : nq0) & 1)))) break;
+        if (!tile && lane == 0) mbar_arrive(&q_empty[buf]);
+        if (g.pair) {
+          if (!(ok = wait(&q_full[buf ^ 1], (uint32_t)((buf ? nq0 : nq1) & 1)))) break;
+          if (lane == 0) mbar_arrive(&q_empty[buf ^ 1]);
+        }
+        __syncwarp();
       }
-      int vst = 0;
+      const int t = tile ? seg_tile(g, x, j) : 0, np = tile ? tile_pages(g, t) : 0;
+      const int n = base_n + t - g.t0;
+      // V up to the tile that is due, then K up to the next tile
+      const int vto = pn >= 0 ? pn : base_n;
+#pragma unroll 1
+      while (vpos < vto && (ok = wait_v())) {
+        if (lane == 0) mbar_arrive(&v_empty[vst]);
+        next_v();
+      }
+      const int kto = tile ? n : have ? base_n + g.t1 - g.t0 : base_n;
+#pragma unroll 1
+      while (ok && kpos < kto && (ok = wait_k())) {
+        if (lane == 0) mbar_arrive(&k_empty[kst]);
+        next_k();
+      }
+      if (!ok || (tile && !(ok = wait_k()))) break;
       if (pn >= 0) {
-        const int use = pn / C::kV;
-        vst = pn - use * C::kV;
-        if (!(ok = wait(&v_full[vst], (uint32_t)(use & 1)))) break;
+        if (!(ok = wait_v())) break;
         // V rows that no query sees (the tails of the last cached page and of the
         // window) become zeros: 0 * NaN would reach every row.  In pair mode both
         // issuers write the same zeros.
@@ -553,7 +580,6 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             if (k < pnp) mma_ts(dO, dS + k * 8, dv + k * (HD * 2), idPV, (k || !pfirst) ? 1u : 0u);
           tc_commit(&pv_done[x]);
           tc_commit(&v_empty[vst]);
-          if (!ppair) tc_commit(&v_empty[vst]);
         }
         if (tile) {
           const uint64_t dq = dq0 + (uint64_t)(buf * C::kQBytes >> 4);
@@ -564,18 +590,15 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             tc_mma_f16(dS, dq + k * 256, dk + k * 16, id, k ? 1u : 0u);
           tc_commit(&s_full[x]);
           tc_commit(&k_empty[kst]);
-          if (!g.pair) tc_commit(&k_empty[kst]);
-          if (j + 1 == (x ? g.nB : g.n)) {  // this stream's last S from this Q
-            tc_commit(&q_empty[buf]);
-            if (g.pair || g.nB == 0) tc_commit(&q_empty[buf]);
-          }
+          if (j + 1 == (x ? g.nB : g.n)) tc_commit(&q_empty[buf]);  // the last S from this Q
         }
       }
       __syncwarp();
+      if (pn >= 0) next_v();
+      if (tile) next_k();
       pn = tile ? n : -1;
       pnp = np;
       pfirst = j == 0;
-      ppair = g.pair;
       pc0 = g.b < 0 ? 0 : g.own_keys - t * kSharedTile;
       pc1 = g.b < 0 ? 0 : g.n_own * kPageBlock - t * kSharedTile + A.W;
     }
@@ -614,6 +637,8 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         float m = x ? m2[1] : m2[0];
         wait(&s_full[x], sph >> x & 1);
         sph ^= 1u << x;
+        // P V of the tile before is in O: done since S was, and every phase is seen
+        if (j > 0) wait(&pv_done[x], (dph >> x & 1) ^ 1u);
         tc_fence_after();
         // what this row does not see becomes -inf, in TMEM and in a rolled loop:
         // only a unit's last tiles need it
@@ -654,8 +679,6 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           const bool raise = mt > m + kRaise;
           if (j > 0) {
             const float a = !raise ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - mt);
-            wait(&pv_done[x], (dph >> x & 1) ^ 1u);  // P V of the tile before is in O
-            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < HD / 2; c += 16) {
               float o[16];
