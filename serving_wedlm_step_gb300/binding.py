@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -100,6 +101,14 @@ class SharedAttnArgs(ctypes.Structure):
         ("workspace_bytes", c_size_t), ("error", c_void_p)]
 
 
+class _Struct(c_void_p):
+    """A struct argument: packed bytes, a ctypes structure by reference, or None."""
+
+    @classmethod
+    def from_param(cls, x):
+        return ctypes.c_char_p(x) if isinstance(x, bytes) else x
+
+
 def load_library(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
@@ -132,9 +141,10 @@ def load_library(path: str = LIB_PATH):
                                   c_int32, POINTER(c_void_p), c_void_p, c_void_p]
     lib.wedlm_generate.argtypes = [c_void_p, POINTER(GenIn), c_void_p]
     lib.wedlm_dual_stream_attention.argtypes = [c_void_p, c_int32, c_int32] + [c_void_p] * 5
-    lib.wedlm_append_kv.argtypes = [POINTER(AppendArgs), c_void_p]
-    lib.wedlm_shared_attention.argtypes = [POINTER(SharedAttnArgs), c_void_p]
-    lib.wedlm_shared_attention_workspace.argtypes = [POINTER(SharedAttnArgs)]
+    # structs as bytes, AppendArgs or SharedAttnArgs by reference, or None
+    lib.wedlm_append_kv.argtypes = [_Struct, c_void_p]
+    lib.wedlm_shared_attention.argtypes = [_Struct, c_void_p]
+    lib.wedlm_shared_attention_workspace.argtypes = [_Struct]
     lib.wedlm_shared_attention_workspace.restype = c_size_t
     return lib
 
@@ -418,53 +428,65 @@ def _bad_arg(msg):
     return WedlmError(ERR_INVALID_ARG, msg)
 
 
+# The two calls below take their structs as packed bytes: filling ctypes fields
+# one by one costs more than the kernels of a small call.  Field order and padding are
+# those of wedlm_append_args and wedlm_shared_attn_args (include/wedlm.h).
+_APPEND_PACK = struct.Struct("@8i2f" + "Pqqq" * 3 + "11P")
+_SHARED_PACK = struct.Struct("@9i4x8PNP")
+_DTYPES = {}
+
+
 def _dtype_code(t):
-    import torch
-    code = {torch.bfloat16: BF16, torch.float32: FP32}.get(t.dtype)
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float32: FP32})
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise _bad_arg(f"tensors are bfloat16 or float32, not {t.dtype}")
     return code
 
 
-def _take(name, t, like, dtype, shape=None, optional=False):
-    """Pointer of a contiguous tensor on `like`'s device, checked."""
+def _take(name, t, dev, dtype, shape=None):
+    """Pointer of a contiguous tensor on CUDA device `dev`, checked; 0 for None."""
     if t is None:
-        if optional:
-            return None
-        raise _bad_arg(f"{name} is missing")
-    if t.device != like.device or t.dtype != dtype or not t.is_contiguous():
-        raise _bad_arg(f"{name} must be a contiguous {dtype} tensor on {like.device}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise _bad_arg(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+        return 0
+    if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+        raise _bad_arg(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
+    if shape is not None and t.shape != shape:
+        raise _bad_arg(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _take_rows(name, t, like, batch, rows):
-    """wedlm_rows of a [batch][rows][heads][head_dim] tensor with dense dims."""
-    if t.device != like.device or t.dtype != like.dtype or t.dim() != 4 or \
-            t.shape[0] != batch or t.shape[1] != rows or t.shape[3] != like.shape[3] or \
+def _take_rows(name, t, dev, dtype, B, n, heads, hd):
+    """Fields of wedlm_rows of a [B][n][heads][hd] tensor whose last dim is dense."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != (B, n, heads, hd) or \
             t.stride(3) != 1:
-        raise _bad_arg(f"{name} must be [{batch}][{rows}][heads][{like.shape[3]}] like k, its "
-                       "last dim dense")
+        raise _bad_arg(f"{name} must be a {dtype} tensor [{B}][{n}][{heads}][{hd}] on cuda:{dev}, "
+                       "its last dim dense")
+    sb, sr, sh, _ = t.stride()
     # a dim of one element has no stride of its own
-    sb, sr, sh = (t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
-    return Rows(t.data_ptr(), sb, sr, sh)
+    return t.data_ptr(), sb if B > 1 else 0, sr if n > 1 else 0, sh if heads > 1 else 0
 
 
 def _pool_pages(pool, n_kv, hd):
-    per = 2 * n_kv * 16 * hd
-    if pool.numel() == 0 or pool.numel() % per:
-        raise _bad_arg(f"the pool must hold whole pages of {per} values")
-    return pool.numel() // per
+    pages, rest = divmod(pool.numel(), 32 * n_kv * hd)
+    if rest or not pages:
+        raise _bad_arg(f"the pool must hold whole pages of {32 * n_kv * hd} values")
+    return pages
 
 
-def _launch(fn, args, device, stream):
-    """Call a context-free entry point on `device`."""
+def _raw_stream(dev, stream):
     import torch
-    if device.index == torch.cuda.current_device():
-        return fn(ctypes.byref(args), _stream_handle(stream))
-    with torch.cuda.device(device):
-        return fn(ctypes.byref(args), _stream_handle(stream))
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _on_device(dev, fn, *args):
+    """Call an entry point that works on the current device on device `dev`."""
+    import torch
+    if torch._C._cuda_getDevice() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def append_kv(k, v, pool, page_table, seq_len, counts=None, pos=None, q=None, q_out=None,
@@ -478,40 +500,36 @@ def append_kv(k, v, pool, page_table, seq_len, counts=None, pos=None, q=None, q_
     layer's pages; page_table int32 [B][max_pages]; seq_len, counts,
     new_seq_len int32 [B]; pos int32 [B][n]; q_out [B*n][n_q][hd]; kv_win
     [B][2][n_kv][Wp*hd]; k_norm, q_norm [hd]; error: int32 [1] that the
-    WEDLM_DEV_* bits are OR-ed into."""
+    WEDLM_DEV_* bits are OR-ed into.  The tensors' device need not be the
+    current one; the stream is that device's current stream, or `stream`."""
     import torch
     if not k.is_cuda or k.dim() != 4:
         raise _bad_arg("k must be a CUDA tensor [B][n][n_kv][hd]")
     B, n, nkv, hd = k.shape
-    if B < 1 or n < 1 or nkv < 1:
+    if not (B and n and nkv and hd):
         raise _bad_arg("k has no rows")
-    code, i32, dt = _dtype_code(k), torch.int32, k.dtype
-    if v.shape != k.shape:
-        raise _bad_arg("v must have the shape of k")
+    dev, dt, i32 = k.get_device(), k.dtype, torch.int32
+    code = _dtype_code(k)
+    if page_table.dim() != 2:
+        raise _bad_arg("page_table must be int32 [B][max_pages]")
     if (q is None) != (q_out is None) or (q is None and q_norm is not None):
         raise _bad_arg("q and q_out go together, and q_norm needs them")
-    nq = 0 if q is None else q.shape[2]
-    wp = (n + 15) // 16 * 16
-    args = AppendArgs(
-        batch=B, rows=n, n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, dtype=code,
-        max_pages_per_seq=page_table.shape[-1], num_pages=_pool_pages(pool, nkv, hd),
-        rms_eps=rms_eps, rope_theta=rope_theta, k=_take_rows("k", k, k, B, n),
-        v=_take_rows("v", v, k, B, n),
-        q_norm=_take("q_norm", q_norm, k, dt, (hd,), True),
-        k_norm=_take("k_norm", k_norm, k, dt, (hd,), True),
-        pos=_take("pos", pos, k, i32, (B, n), True),
-        counts=_take("counts", counts, k, i32, (B,), True),
-        seq_len=_take("seq_len", seq_len, k, i32, (B,)),
-        page_table=_take("page_table", page_table, k, i32, (B, page_table.shape[-1])),
-        kv_pool=_take("pool", pool, k, dt),
-        new_seq_len=_take("new_seq_len", new_seq_len, k, i32, (B,), True),
-        error=_take("error", error, k, i32, (1,), True))
+    cols = page_table.shape[1]
+    nq, q_rows = 0, (0, 0, 0, 0)
     if q is not None:
-        args.q = _take_rows("q", q, k, B, n)
-        args.q_out = _take("q_out", q_out, k, dt, (B * n, nq, hd))
-    if kv_win is not None:
-        args.kv_win = _take("kv_win", kv_win, k, dt, (B, 2, nkv, wp * hd))
-    rc = _launch(lib().wedlm_append_kv, args, k.device, stream)
+        nq = q.shape[2] if q.dim() == 4 else 0
+        q_rows = _take_rows("q", q, dev, dt, B, n, nq, hd)
+    args = _APPEND_PACK.pack(
+        B, n, nq, nkv, hd, code, cols, _pool_pages(pool, nkv, hd), rms_eps, rope_theta,
+        *_take_rows("k", k, dev, dt, B, n, nkv, hd), *_take_rows("v", v, dev, dt, B, n, nkv, hd),
+        *q_rows, _take("q_norm", q_norm, dev, dt, (hd,)), _take("k_norm", k_norm, dev, dt, (hd,)),
+        _take("pos", pos, dev, i32, (B, n)), _take("counts", counts, dev, i32, (B,)),
+        _take("seq_len", seq_len, dev, i32, (B,)),
+        _take("page_table", page_table, dev, i32, (B, cols)), _take("pool", pool, dev, dt),
+        _take("q_out", q_out, dev, dt, (B * n, nq, hd)),
+        _take("kv_win", kv_win, dev, dt, (B, 2, nkv, (n + 15) // 16 * 16 * hd)),
+        _take("new_seq_len", new_seq_len, dev, i32, (B,)), _take("error", error, dev, i32, (1,)))
+    rc = _on_device(dev, lib().wedlm_append_kv, args, _raw_stream(dev, stream))
     if rc != OK:
         raise WedlmError(rc, "wedlm_append_kv failed")
 
@@ -525,37 +543,31 @@ def shared_prefix_attention(q, pool, shared_pages, page_table, seq_len, kv_win, 
     [B][max_pages]; seq_len int32 [B], shared part included; kv_win
     [B][2][n_kv][Wp*hd]; o: [B*W][n_q*hd], returned.  workspace: a byte tensor
     of at least shared_prefix_workspace() bytes that no overlapping call uses;
-    by default one is taken from torch's allocator, on the call's stream."""
+    by default one is taken from torch's allocator, on the call's stream.  The
+    tensors' device need not be the current one."""
     import torch
-    if not q.is_cuda or q.dim() != 3 or kv_win.dim() != 4 or seq_len.dim() != 1:
-        raise _bad_arg("q must be a CUDA tensor [B*W][n_q][hd], kv_win [B][2][n_kv][Wp*hd]")
+    if not q.is_cuda or q.dim() != 3 or kv_win.dim() != 4 or seq_len.dim() != 1 or \
+            page_table.dim() != 2:
+        raise _bad_arg("q must be a CUDA tensor [B*W][n_q][hd], kv_win [B][2][n_kv][Wp*hd], "
+                       "seq_len [B], page_table [B][max_pages]")
     (M, nq, hd), B, nkv = q.shape, seq_len.shape[0], kv_win.shape[2]
-    if B < 1 or M < 1 or M % B or nkv < 1:
+    if not (B and M and nq and hd and nkv) or M % B:
         raise _bad_arg("q must have W >= 1 rows for every sequence")
-    W, i32, dt, code = M // B, torch.int32, q.dtype, _dtype_code(q)
-    wp = (W + 15) // 16 * 16
-    S = 0 if shared_pages is None else shared_pages.shape[0]
-    args = SharedAttnArgs(
-        batch=B, window=W, n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, dtype=code,
-        n_shared_pages=S, max_pages_per_seq=page_table.shape[-1],
-        num_pages=_pool_pages(pool, nkv, hd), q=_take("q", q, q, dt),
-        kv_pool=_take("pool", pool, q, dt),
-        shared_pages=_take("shared_pages", shared_pages, q, i32, (S,), True) if S else None,
-        page_table=_take("page_table", page_table, q, i32, (B, page_table.shape[-1])),
-        seq_len=_take("seq_len", seq_len, q, i32, (B,)),
-        kv_win=_take("kv_win", kv_win, q, dt, (B, 2, nkv, wp * hd)),
-        o=_take("o", o, q, dt, (M, nq * hd)), error=_take("error", error, q, i32, (1,), True))
-    if q.device.index != torch.cuda.current_device():
-        with torch.cuda.device(q.device):
-            return _shared_prefix_attention(args, q, o, workspace, stream)
-    return _shared_prefix_attention(args, q, o, workspace, stream)
-
-
-def _shared_prefix_attention(args, q, o, workspace, stream):
-    import torch
+    W, dev, dt, i32 = M // B, q.get_device(), q.dtype, torch.int32
+    code = _dtype_code(q)
+    S, cols = 0 if shared_pages is None else shared_pages.numel(), page_table.shape[1]
+    sizes = (B, W, nq, nkv, hd, code, S, cols, _pool_pages(pool, nkv, hd))
+    ptrs = (_take("q", q, dev, dt), _take("pool", pool, dev, dt),
+            _take("shared_pages", shared_pages, dev, i32, (S,)) if S else 0,
+            _take("page_table", page_table, dev, i32, (B, cols)),
+            _take("seq_len", seq_len, dev, i32, (B,)),
+            _take("kv_win", kv_win, dev, dt, (B, 2, nkv, (W + 15) // 16 * 16 * hd)),
+            _take("o", o, dev, dt, (M, nq * hd)))
+    err = _take("error", error, dev, i32, (1,))
     L = lib()
     if workspace is None:
-        need = L.wedlm_shared_attention_workspace(ctypes.byref(args))
+        need = L.wedlm_shared_attention_workspace(
+            _SHARED_PACK.pack(*sizes, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0))
         if need == 0:
             raise _bad_arg("sizes that wedlm_shared_attention does not take")
         if stream is None:
@@ -563,11 +575,11 @@ def _shared_prefix_attention(args, q, o, workspace, stream):
         else:  # freed on return: its next user must come after this call on its stream
             with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
-        raise _bad_arg(f"workspace must be a contiguous tensor on {q.device}")
-    args.workspace = workspace.data_ptr()
-    args.workspace_bytes = workspace.numel() * workspace.element_size()
-    rc = L.wedlm_shared_attention(ctypes.byref(args), _stream_handle(stream))
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise _bad_arg(f"workspace must be a contiguous tensor on cuda:{dev}")
+    args = _SHARED_PACK.pack(*sizes, *ptrs, workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), err)
+    rc = _on_device(dev, L.wedlm_shared_attention, args, _raw_stream(dev, stream))
     if rc != OK:
         raise WedlmError(rc, "wedlm_shared_attention failed")
     return o
@@ -580,7 +592,7 @@ def shared_prefix_workspace(batch, window, n_q_heads, n_kv_heads, head_dim, dtyp
     args = SharedAttnArgs(batch=batch, window=window, n_q_heads=n_q_heads, n_kv_heads=n_kv_heads,
                           head_dim=head_dim, dtype=dtype, n_shared_pages=n_shared_pages,
                           max_pages_per_seq=max_pages_per_seq, num_pages=1)
-    need = lib().wedlm_shared_attention_workspace(ctypes.byref(args))
+    need = lib().wedlm_shared_attention_workspace(bytes(args))
     if need == 0:
         raise _bad_arg("sizes that wedlm_shared_attention does not take")
     return need

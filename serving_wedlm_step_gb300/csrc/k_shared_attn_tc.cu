@@ -637,8 +637,10 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         float m = x ? m2[1] : m2[0];
         wait(&s_full[x], sph >> x & 1);
         sph ^= 1u << x;
-        // P V of the tile before is in O: done since S was, and every phase is seen
-        if (j > 0) wait(&pv_done[x], (dph >> x & 1) ^ 1u);
+        // P V of the tile before is in O: done since S was, but every phase is seen
+        // (asked here, answered below, behind the loads of S)
+        const uint32_t pv_ph = (dph >> x & 1) ^ 1u;
+        const bool pv_ok = j == 0 || mbar_try_wait(&pv_done[x], pv_ph);
         tc_fence_after();
         // what this row does not see becomes -inf, in TMEM and in a rolled loop:
         // only a unit's last tiles need it
@@ -670,6 +672,10 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         float mt = max64(v) * sc;
         // Does a row of either warp raise its maximum?  The meeting also keeps P
         // from S columns the other warp has not read yet.
+        if (!__all_sync(0xffffffffu, pv_ok)) {
+          wait(&pv_done[x], pv_ph);
+          tc_fence_after();
+        }
         const int odd = ++tiles & 1;  // one of the two may be a tile ahead: two sets
         s_red[odd][h][r] = mt;
         if (__any_sync(0xffffffffu, mt > m + kRaise)) s_raise[odd][q] = tiles;
