@@ -62,7 +62,7 @@ template <int HD> struct Cfg {
   static constexpr uint32_t kQBytes = 128 * HD * 2;
   // tiles in flight: what fits beside Q; K is needed before V
   static constexpr int kK = HD == 128 ? 3 : 4, kV = HD == 128 ? 2 : 4;
-  static constexpr uint32_t kSmem = 2 * kQBytes + (kK + kV) * kTileBytes + 128;
+  static constexpr uint32_t kData = 2 * kQBytes + (kK + kV) * kTileBytes;
 };
 
 // A segment as the planner publishes it; n = 0 ends the list.
@@ -130,16 +130,6 @@ __device__ __forceinline__ void ld64(uint32_t taddr, float* v) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
-      "[%32];\n\ttcgen05.wait::ld.sync.aligned;"
-      : R8(v, 0), R8(v, 8), R8(v, 16), R8(v, 24)
-      : "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void ld16(uint32_t taddr, float* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -152,15 +142,6 @@ __device__ __forceinline__ void ld16(uint32_t taddr, float* v) {
 #undef R8
 #define W8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), \
                  "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
-__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
-          taddr),
-      W8(r, 0), W8(r, 8), W8(r, 16), W8(r, 24)
-      : "memory");
-}
 __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -198,13 +179,13 @@ __device__ __forceinline__ float max64(const float* v) {
   }
   return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
-// p = 2^(v * sc + nm) of 64 columns to 32 columns of bf16 pairs; their sum
-__device__ __forceinline__ float exp64(uint32_t taddr, const float* v, float sc, float nm) {
+// p = 2^(v * sc + nm) of 32 columns to 16 columns of bf16 pairs; their sum
+__device__ __forceinline__ float exp32(uint32_t taddr, const float* v, float sc, float nm) {
   const uint64_t sc2 = pack2(sc, sc), nm2 = pack2(nm, nm);
   uint64_t ps[2] = {0, 0};
-  uint32_t pk[32];
+  uint32_t pk[16];
 #pragma unroll
-  for (int c = 0; c < 64; c += 2) {
+  for (int c = 0; c < 32; c += 2) {
     float p0, p1;
     unpack2(fma2(pack2(v[c], v[c + 1]), sc2, nm2), p0, p1);
     p0 = ex2_approx(p0);
@@ -213,7 +194,7 @@ __device__ __forceinline__ float exp64(uint32_t taddr, const float* v, float sc,
     const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
     pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
   }
-  st32(taddr, pk);
+  st16(taddr, pk);
   float s0, s1;
   unpack2(add2(ps[0], ps[1]), s0, s1);
   return s0 + s1;
@@ -221,6 +202,20 @@ __device__ __forceinline__ float exp64(uint32_t taddr, const float* v, float sc,
 __device__ __forceinline__ void wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+
+template <int HD> struct Ctl {
+  uint64_t k_full[Cfg<HD>::kK], k_empty[Cfg<HD>::kK], v_full[Cfg<HD>::kV], v_empty[Cfg<HD>::kV];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t pair[4], fin;  // pair: the two softmax warps of a row
+  Seg seg[kSegs];
+  const bf16* src[2][kSharedTilePages];  // a tile's pages: K, V
+  float red[2][2][128];                  // [half][row]: row max of a tile; at the end, row sums
+  int raise[2][4];                       // [tile parity]: last tile that raised a maximum
+  int issued[4];                         // copies of K, V, Q buffer 0 and 1 started
+  int abort;
+  uint32_t tmem;
+};
 
 // the slow half of a wait, written once; false when this or another wait expired
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err,
@@ -245,72 +240,63 @@ __global__ void __launch_bounds__(kThreads, 1)
 shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ SharedArgs A,
                       int TPB) {
   using C = Cfg<HD>;
-  extern __shared__ uint8_t dsm[];
-  __shared__ __align__(8) uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV];
-  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
-  __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], joined[4], fin;
-  __shared__ Seg s_seg[kSegs];
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_issued[4];  // copies of K, V, Q buffer 0 and 1 started
-  __shared__ __align__(16) const bf16* s_src[2][kSharedTilePages];
-  __shared__ float s_red[2][2][128];  // [half][row]: row max of a tile; at the end, row sums
-  __shared__ int s_raise[2][4];                       // last tile that raised a maximum
-
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 127) &
-                                             ~static_cast<uintptr_t>(127));
+  // no static shared memory: the data starts on a 1024-byte boundary, as the
+  // swizzled rows of Q need, and fills the SM's 227 KB up to the control block
+  extern __shared__ __align__(1024) uint8_t base[];
   uint8_t* k_ring = base + 2 * C::kQBytes;
   uint8_t* v_ring = k_ring + C::kK * C::kTileBytes;
+  Ctl<HD>& ctl = *reinterpret_cast<Ctl<HD>*>(base + C::kData);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = A.G;
 
   if (threadIdx.x == 32) {
     for (int i = 0; i < C::kK; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 2);  // both issuers
+      mbar_init(&ctl.k_full[i], 1);
+      mbar_init(&ctl.k_empty[i], 2);  // both issuers
     }
     for (int i = 0; i < C::kV; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 2);
+      mbar_init(&ctl.v_full[i], 1);
+      mbar_init(&ctl.v_empty[i], 2);
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&q_full[x], 1);
-      mbar_init(&q_empty[x], 2);
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 8);
-      mbar_init(&pv_done[x], 1);
+      mbar_init(&ctl.q_full[x], 1);
+      mbar_init(&ctl.q_empty[x], 2);
+      mbar_init(&ctl.s_full[x], 1);
+      mbar_init(&ctl.p_full[x], 8);
+      mbar_init(&ctl.pv_done[x], 1);
     }
     for (int i = 0; i < kSegs; ++i) {
-      mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 12);  // copiers, issuers, 8 softmax warps
-      mbar_init(&joined[i], 2);
-      s_issued[i] = s_raise[0][i] = s_raise[1][i] = 0;
+      mbar_init(&ctl.seg_full[i], 1);
+      mbar_init(&ctl.seg_empty[i], 12);  // copiers, issuers, 8 softmax warps
+      mbar_init(&ctl.pair[i], 2);
+      ctl.issued[i] = ctl.raise[0][i] = ctl.raise[1][i] = 0;
     }
-    mbar_init(&fin, 2);
-    s_abort = 0;
+    mbar_init(&ctl.fin, 2);
+    ctl.abort = 0;
     mbar_fence_init();
   }
   if (warp == 0) {
-    tmem_alloc(&s_tmem, kTmemCols);
+    tmem_alloc(&ctl.tmem, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = ctl.tmem;
   // warp-wide and bounded (2 s): what follows is executed by the whole warp together
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     bool ok = mbar_try_wait(bar, parity);
-    if (!ok) ok = wait_on(bar, parity, A.err, &s_abort);
+    if (!ok) ok = wait_on(bar, parity, A.err, &ctl.abort);
     return __all_sync(0xffffffffu, ok);
   };
   // next published segment, into registers (warp-wide); false after the last
   int seg_i = 0, pub_i = 0;
   uint32_t seg_ph = 0, pub_ph = 0;
   auto get = [&](Seg& g) -> bool {
-    if (!wait(&seg_full[seg_i], seg_ph)) return false;
-    g = s_seg[seg_i];
+    if (!wait(&ctl.seg_full[seg_i], seg_ph)) return false;
+    g = ctl.seg[seg_i];
     __syncwarp();
-    if (lane == 0) mbar_arrive(&seg_empty[seg_i]);
+    if (lane == 0) mbar_arrive(&ctl.seg_empty[seg_i]);
     if (++seg_i == kSegs) {
       seg_i = 0;
       seg_ph ^= 1u;
@@ -323,8 +309,8 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   if (warp == 8 || warp == 10) {
     // ---------------- copiers: Q and K (8), V (10); 10 plans too ----------------
     const int kv = warp == 10;
-    uint64_t* full = kv ? v_full : k_full;
-    uint64_t* empty = kv ? v_empty : k_empty;
+    uint64_t* full = kv ? ctl.v_full : ctl.k_full;
+    uint64_t* empty = kv ? ctl.v_empty : ctl.k_empty;
     uint8_t* ring = kv ? v_ring : k_ring;
     const int NS = kv ? C::kV : C::kK;
     const uint64_t keep = l2_evict_last_policy(), once = l2_evict_first_policy();
@@ -361,10 +347,10 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         g.slot = seg_slot(A, u.unit, blockIdx.x);
       }
       planned = !more;
-      if (!wait(&seg_empty[pub_i], pub_ph ^ 1u)) return false;
+      if (!wait(&ctl.seg_empty[pub_i], pub_ph ^ 1u)) return false;
       if (lane == 0) {
-        s_seg[pub_i] = g;
-        mbar_arrive(&seg_full[pub_i]);
+        ctl.seg[pub_i] = g;
+        mbar_arrive(&ctl.seg_full[pub_i]);
         if (more) record_unit(A, u);
       }
       __syncwarp();
@@ -403,14 +389,14 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       for (int x = 0; !kv && x < 1 + g.pair; ++x) {
         const int buf = g.pair ? x : flip;
         const int nq = buf ? nq1++ : nq0++;
-        if (!(ok = wait(&q_empty[buf], (uint32_t)(nq & 1) ^ 1u))) break;
+        if (!(ok = wait(&ctl.q_empty[buf], (uint32_t)(nq & 1) ^ 1u))) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&q_full[buf], (uint32_t)(min(TPB, A.B * A.W) * G) * HD * 2);
+          mbar_arrive_expect_tx(&ctl.q_full[buf], (uint32_t)(min(TPB, A.B * A.W) * G) * HD * 2);
 #pragma unroll 1
-          for (int c = 0; c < HD / 8; ++c)
-            load_q_box(base + buf * C::kQBytes + c * 2048, &mq, &q_full[buf], 8 * c, g.kvh * G,
-                       g.tok0 + x * TPB);
-          s_issued[2 + buf] = nq + 1;
+          for (int c = 0; c < HD / 64; ++c)
+            load_q_box(base + buf * C::kQBytes + c * 128 * 128, &mq, &ctl.q_full[buf], 64 * c,
+                       g.kvh * G, g.tok0 + x * TPB);
+          ctl.issued[2 + buf] = nq + 1;
         }
         __syncwarp();
       }
@@ -429,7 +415,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           else
             set_err(A.err, WEDLM_DEV_BAD_PAGE);
         }
-        if (lane < kSharedTilePages) s_src[kv][lane] = src;
+        if (lane < kSharedTilePages) ctl.src[kv][lane] = src;
         const unsigned have = __ballot_sync(0xffffffffu, src != nullptr);
         if (!(ok = wait(&empty[st], ph))) break;
         uint8_t* dst = ring + st * C::kTileBytes;
@@ -448,16 +434,16 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           if (have == (1u << kSharedTilePages) - 1) {
             const bf16* sp[kSharedTilePages];
 #pragma unroll
-            for (int p = 0; p < kSharedTilePages; ++p) sp[p] = s_src[kv][p];
+            for (int p = 0; p < kSharedTilePages; ++p) sp[p] = ctl.src[kv][p];
 #pragma unroll
             for (int p = 0; p < kSharedTilePages; ++p)
               bulk_load(dst + p * C::kPage, sp[p], C::kPage, bar, pol);
           } else {
 #pragma unroll 1
             for (int p = 0; p < kSharedTilePages; ++p)
-              if (have >> p & 1) bulk_load(dst + p * C::kPage, s_src[kv][p], C::kPage, bar, pol);
+              if (have >> p & 1) bulk_load(dst + p * C::kPage, ctl.src[kv][p], C::kPage, bar, pol);
           }
-          s_issued[kv] = ++issued;
+          ctl.issued[kv] = ++issued;
         }
         __syncwarp();
         if (++st == NS) {
@@ -469,10 +455,11 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     }
   } else if (warp == 9 || warp == 11) {
     // ---------------- MMA issuers ----------------
-    // Q: 8-dim groups 2048 B apart, 8-row groups 128 B; K: 128 B and HD*16 B
-    // (K-major); V: 8-token groups HD*16 B apart, 8-dim groups 128 B (MN-major)
+    // Q: rows of 64 dims, 128-byte swizzle (16 KB a half; 16 dims are 32 bytes); K:
+    // 8-dim groups 128 B and 8-token groups HD*16 B apart (K-major); V: 8-token
+    // groups HD*16 B, 8-dim groups 128 B apart (MN-major)
     const int x = warp == 11;
-    const uint64_t dq0 = sdesc_noswz(smem_u32(base), 2048, 128);
+    const uint64_t dq0 = sdesc_sw128(smem_u32(base));
     const uint64_t dk0 = sdesc_noswz(smem_u32(k_ring), 128, HD * 16);
     const uint64_t dv0 = sdesc_noswz(smem_u32(v_ring), HD * 16, 128);
     const uint32_t idPV = idesc_bf16_m128(HD) | (1u << 16);
@@ -486,8 +473,8 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     // parity tells two neighbouring phases apart, so a reader may not skip any.
     int kpos = 0, vpos = 0, kst = 0, vst = 0;
     uint32_t kph = 0, vph = 0;
-    auto wait_k = [&]() { return wait(&k_full[kst], kph); };
-    auto wait_v = [&]() { return wait(&v_full[vst], vph); };
+    auto wait_k = [&]() { return wait(&ctl.k_full[kst], kph); };
+    auto wait_v = [&]() { return wait(&ctl.v_full[vst], vph); };
     auto next_k = [&]() {
       ++kpos;
       if (++kst == C::kK) {
@@ -525,11 +512,11 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       const bool tile = have && j < (x ? g.nB : g.n);
       const int buf = g.pair ? x : flip;
       if (have && j == 0) {  // a new segment's Q
-        if (!(ok = wait(&q_full[buf], (uint32_t)((buf ? nq1 : nq0) & 1)))) break;
-        if (!tile && lane == 0) mbar_arrive(&q_empty[buf]);
+        if (!(ok = wait(&ctl.q_full[buf], (uint32_t)((buf ? nq1 : nq0) & 1)))) break;
+        if (!tile && lane == 0) mbar_arrive(&ctl.q_empty[buf]);
         if (g.pair) {
-          if (!(ok = wait(&q_full[buf ^ 1], (uint32_t)((buf ? nq0 : nq1) & 1)))) break;
-          if (lane == 0) mbar_arrive(&q_empty[buf ^ 1]);
+          if (!(ok = wait(&ctl.q_full[buf ^ 1], (uint32_t)((buf ? nq0 : nq1) & 1)))) break;
+          if (lane == 0) mbar_arrive(&ctl.q_empty[buf ^ 1]);
         }
         __syncwarp();
       }
@@ -539,13 +526,13 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       const int vto = pn >= 0 ? pn : base_n;
 #pragma unroll 1
       while (vpos < vto && (ok = wait_v())) {
-        if (lane == 0) mbar_arrive(&v_empty[vst]);
+        if (lane == 0) mbar_arrive(&ctl.v_empty[vst]);
         next_v();
       }
       const int kto = tile ? n : have ? base_n + g.t1 - g.t0 : base_n;
 #pragma unroll 1
       while (ok && kpos < kto && (ok = wait_k())) {
-        if (lane == 0) mbar_arrive(&k_empty[kst]);
+        if (lane == 0) mbar_arrive(&ctl.k_empty[kst]);
         next_k();
       }
       if (!ok || (tile && !(ok = wait_k()))) break;
@@ -568,7 +555,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                   make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
-        if (!(ok = wait(&p_full[x], pph))) break;
+        if (!(ok = wait(&ctl.p_full[x], pph))) break;
         pph ^= 1u;
       }
       if (elect_one()) {
@@ -578,8 +565,8 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 #pragma unroll
           for (int k = 0; k < kSharedTilePages; ++k)  // 16 keys: 8 columns of P
             if (k < pnp) mma_ts(dO, dS + k * 8, dv + k * (HD * 2), idPV, (k || !pfirst) ? 1u : 0u);
-          tc_commit(&pv_done[x]);
-          tc_commit(&v_empty[vst]);
+          tc_commit(&ctl.pv_done[x]);
+          tc_commit(&ctl.v_empty[vst]);
         }
         if (tile) {
           const uint64_t dq = dq0 + (uint64_t)(buf * C::kQBytes >> 4);
@@ -587,10 +574,11 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           const uint32_t id = idesc_bf16_m128(np * kPageBlock);
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k)  // 16 dims: two 8-dim groups
-            tc_mma_f16(dS, dq + k * 256, dk + k * 16, id, k ? 1u : 0u);
-          tc_commit(&s_full[x]);
-          tc_commit(&k_empty[kst]);
-          if (j + 1 == (x ? g.nB : g.n)) tc_commit(&q_empty[buf]);  // the last S from this Q
+            tc_mma_f16(dS, dq + (k / 4) * (128 * 128 / 16) + (k % 4) * 2, dk + k * 16, id,
+                       k ? 1u : 0u);
+          tc_commit(&ctl.s_full[x]);
+          tc_commit(&ctl.k_empty[kst]);
+          if (j + 1 == (x ? g.nB : g.n)) tc_commit(&ctl.q_empty[buf]);  // the last S from this Q
         }
       }
       __syncwarp();
@@ -603,8 +591,8 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       pc1 = g.b < 0 ? 0 : g.n_own * kPageBlock - t * kSharedTile + A.W;
     }
     // every MMA has completed before TMEM is freed
-    if (elect_one()) tc_commit(&fin);
-    mbar_wait(&fin, 0, A.err);
+    if (elect_one()) tc_commit(&ctl.fin);
+    mbar_wait(&ctl.fin, 0, A.err);
   } else {
     // ---------------- softmax ----------------
     // Warps q and q+4 hold query rows 32q .. 32q+31 of both streams (thread = row):
@@ -613,13 +601,13 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     const int r = 32 * q + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
     const float sc = A.scale_log2;
-    uint32_t sph = 0, dph = 0, jph = 0;  // phases: bit x of s_full and pv_done, of the pair's
+    uint32_t sph = 0, dph = 0, jph = 0;  // phases: bit x of ctl.s_full and ctl.pv_done, of the pair's
     // The two warps of a row meet.  An mbarrier and not a named one, so that a wait
     // that expired elsewhere cannot leave one of them here for good.
     auto pair_sync = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&joined[q]);
-      wait(&joined[q], jph);
+      if (lane == 0) mbar_arrive(&ctl.pair[q]);
+      wait(&ctl.pair[q], jph);
       jph ^= 1u;
     };
     Seg g;
@@ -635,12 +623,12 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         const uint32_t tS = tl + kColS + (uint32_t)(x * 128);
         const uint32_t tO = tl + kColO + (uint32_t)(x * 128 + h * (HD / 2));
         float m = x ? m2[1] : m2[0];
-        wait(&s_full[x], sph >> x & 1);
+        wait(&ctl.s_full[x], sph >> x & 1);
         sph ^= 1u << x;
         // P V of the tile before is in O: done since S was, but every phase is seen
         // (asked here, answered below, behind the loads of S)
         const uint32_t pv_ph = (dph >> x & 1) ^ 1u;
-        const bool pv_ok = j == 0 || mbar_try_wait(&pv_done[x], pv_ph);
+        const bool pv_ok = j == 0 || mbar_try_wait(&ctl.pv_done[x], pv_ph);
         tc_fence_after();
         // what this row does not see becomes -inf, in TMEM and in a rolled loop:
         // only a unit's last tiles need it
@@ -673,15 +661,15 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         // Does a row of either warp raise its maximum?  The meeting also keeps P
         // from S columns the other warp has not read yet.
         if (!__all_sync(0xffffffffu, pv_ok)) {
-          wait(&pv_done[x], pv_ph);
+          wait(&ctl.pv_done[x], pv_ph);
           tc_fence_after();
         }
         const int odd = ++tiles & 1;  // one of the two may be a tile ahead: two sets
-        s_red[odd][h][r] = mt;
-        if (__any_sync(0xffffffffu, mt > m + kRaise)) s_raise[odd][q] = tiles;
+        ctl.red[odd][h][r] = mt;
+        if (__any_sync(0xffffffffu, mt > m + kRaise)) ctl.raise[odd][q] = tiles;
         pair_sync();
-        if (s_raise[odd][q] == tiles) {
-          mt = fmaxf(mt, s_red[odd][h ^ 1][r]);
+        if (ctl.raise[odd][q] == tiles) {
+          mt = fmaxf(mt, ctl.red[odd][h ^ 1][r]);
           const bool raise = mt > m + kRaise;
           if (j > 0) {
             const float a = !raise ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - mt);
@@ -699,29 +687,30 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           if (raise) m = mt;
           if (x) m2[1] = m; else m2[0] = m;
         }
-        const float ps = exp64(tS + h * 32, v, sc, m == -INFINITY ? 0.f : -m);
+        const float nm = m == -INFINITY ? 0.f : -m;
+        const float ps = exp32(tS + h * 32, v, sc, nm) + exp32(tS + h * 32 + 16, v + 32, sc, nm);
         if (x) l2[1] += ps; else l2[0] += ps;
         wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (lane == 0) mbar_arrive(&ctl.p_full[x]);
         dph ^= 1u << x;
       }
       // The segment's partial: O once its last P V is done.  Pair: this warp's half
       // of the dims of both streams' rows.  Split: A and B joined.
-      wait(&pv_done[0], (dph & 1) ^ 1u);
-      if (g.nB > 0) wait(&pv_done[1], (dph >> 1) ^ 1u);
+      wait(&ctl.pv_done[0], (dph & 1) ^ 1u);
+      if (g.nB > 0) wait(&ctl.pv_done[1], (dph >> 1) ^ 1u);
       tc_fence_after();
-      pair_sync();  // the other warp is done with s_red too
-      s_red[h][0][r] = l2[0];  // the row sums are in halves
-      s_red[h][1][r] = l2[1];
+      pair_sync();  // the other warp is done with `red` too
+      ctl.red[h][0][r] = l2[0];  // the row sums are in halves
+      ctl.red[h][1][r] = l2[1];
       pair_sync();
       const int urows = g.b < 0 ? A.srows : A.prows;
       float4* po = (g.b < 0 ? A.part_s : A.part_p) +
                    ((size_t)g.slot * (HD / 4) + h * (HD / 8)) * urows;
       float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + (size_t)g.slot * urows;
       float f[2] = {1.f, 1.f};
-      const float la = l2[0] + s_red[h ^ 1][0][r], lb = l2[1] + s_red[h ^ 1][1][r];
+      const float la = l2[0] + ctl.red[h ^ 1][0][r], lb = l2[1] + ctl.red[h ^ 1][1][r];
       if (!g.pair) {
         const float M = fmaxf(m2[0], m2[1]);
         f[0] = m2[0] == -INFINITY ? 0.f : ex2_approx(m2[0] - M);
@@ -759,24 +748,24 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         }
       }
       tc_fence_before();
-      pair_sync();  // s_red may be written again
+      pair_sync();  // `red` may be written again
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (s_abort && threadIdx.x == 256) {
+  if (ctl.abort && threadIdx.x == 256) {
     // a wait expired: let the copies still in flight land (bounded; a phase that
     // has passed answers at once)
 #pragma unroll 1
-    for (int i = max(0, s_issued[0] - C::kK); i < s_issued[0]; ++i)
-      mbar_wait(&k_full[i % C::kK], (uint32_t)(i / C::kK) & 1u, A.err);
+    for (int i = max(0, ctl.issued[0] - C::kK); i < ctl.issued[0]; ++i)
+      mbar_wait(&ctl.k_full[i % C::kK], (uint32_t)(i / C::kK) & 1u, A.err);
 #pragma unroll 1
-    for (int i = max(0, s_issued[1] - C::kV); i < s_issued[1]; ++i)
-      mbar_wait(&v_full[i % C::kV], (uint32_t)(i / C::kV) & 1u, A.err);
+    for (int i = max(0, ctl.issued[1] - C::kV); i < ctl.issued[1]; ++i)
+      mbar_wait(&ctl.v_full[i % C::kV], (uint32_t)(i / C::kV) & 1u, A.err);
 #pragma unroll 1
     for (int x = 0; x < 2; ++x)
-      if (s_issued[2 + x]) mbar_wait(&q_full[x], (uint32_t)(s_issued[2 + x] - 1) & 1u, A.err);
+      if (ctl.issued[2 + x]) mbar_wait(&ctl.q_full[x], (uint32_t)(ctl.issued[2 + x] - 1) & 1u, A.err);
   }
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
@@ -800,23 +789,26 @@ template <int HD>
 cudaError_t launch(const SharedArgs& A, int TPB, cudaStream_t st) {
   const auto enc = encoder();
   if (!enc) return cudaErrorNotSupported;
-  // q as {dim, head, token}: a box of 8 dims, G heads and TPB tokens is one 8-dim
-  // group of a row block, rows token * G + g
+  // q as {dim, head, token}: a box of 64 dims, G heads and TPB tokens is half (all) of
+  // a row block, rows token * G + g of 128 bytes.  (Boxes of 8 dims, laid out like K,
+  // are 16-byte pieces: a pair of row blocks took 5,000 cycles to arrive.)
   CUtensorMap mq;
   const cuuint64_t nq = (cuuint64_t)A.nkv * A.G;
   cuuint64_t dims[3] = {HD, nq, (cuuint64_t)A.B * A.W};
   cuuint64_t strides[2] = {HD * 2, nq * HD * 2};
-  cuuint32_t box[3] = {8, (cuuint32_t)A.G, (cuuint32_t)std::min(TPB, A.B * A.W)};
+  cuuint32_t box[3] = {64, (cuuint32_t)A.G, (cuuint32_t)std::min(TPB, A.B * A.W)};
   cuuint32_t one[3] = {1, 1, 1};
   if (enc(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(A.q), dims, strides, box, one,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
+  constexpr size_t kSmem = Cfg<HD>::kData + sizeof(Ctl<HD>);
+  static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
   const cudaError_t e = cudaFuncSetAttribute(shared_attn_tc_kernel<HD>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)Cfg<HD>::kSmem);
+                                             (int)kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(shared_attn_tc_kernel<HD>, dim3(A.grid), dim3(kThreads), Cfg<HD>::kSmem, st, mq,
+  return launch_pdl(shared_attn_tc_kernel<HD>, dim3(A.grid), dim3(kThreads), kSmem, st, mq,
                     A, TPB);
 }
 
