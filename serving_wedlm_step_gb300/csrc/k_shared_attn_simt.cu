@@ -1,4 +1,4 @@
-// Shared-prefix window attention on the CUDA cores, and the merge of the
+// Shared-prefix window attention on the CUDA cores (fp32), and the merge of the
 // partials of either kernel.
 //
 // One pass over a segment's keys with the running maximum m and sum l of each
@@ -21,8 +21,9 @@ template <int HD> constexpr int simt_smem_bytes() {
   return ((kSimtRows + 2 * kSharedTile) * (HD + 4) + kSimtRows * kPRow) * (int)sizeof(float);
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedArgs A) {
+template <int HD>
+__global__ void __launch_bounds__(kSimtThreads)
+shared_attn_simt_kernel(const __grid_constant__ SharedArgs A) {
   constexpr int LD = HD + 4, ND = HD / 64;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;                        // [64][LD], scaled
@@ -31,6 +32,8 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
   float* Ps = Vs + kSharedTile * LD;     // [64][kPRow]
   __shared__ SharedSeg s_seg;
   __shared__ bool s_more;
+  __shared__ const float* s_page[2 * kSharedTilePages];
+  __shared__ int s_seen[2 * kSharedTilePages];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -57,15 +60,18 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
     const int all_rows = (g.b < 0 ? A.B : 1) * A.W * A.G;
     const int row0 = g.blk * urows, nrows = min(urows, all_rows - row0);
     const int tok0 = g.b < 0 ? 0 : g.b * A.W;
-    const T* q = static_cast<const T*>(A.q);
-    for (int e = tid; e < kSimtRows * HD; e += kSimtThreads) {
-      const int r = e / HD, d = e % HD;
-      float v = 0.f;
+    const float* q = static_cast<const float*>(A.q);
+#pragma unroll
+    for (int i = 0; i < kSimtRows * HD / 4 / kSimtThreads; ++i) {
+      const int e = tid + i * kSimtThreads, r = e / (HD / 4), d = e % (HD / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < nrows) {
         const int row = row0 + r;
-        v = to_f(q[((size_t)(tok0 + row / A.G) * nq + g.kvh * A.G + row % A.G) * HD + d]);
+        v = *reinterpret_cast<const float4*>(
+            q + ((size_t)(tok0 + row / A.G) * nq + g.kvh * A.G + row % A.G) * HD + d);
       }
-      Qs[r * LD + d] = v * A.scale_log2;
+      *reinterpret_cast<float4*>(Qs + r * LD + d) = make_float4(
+          v.x * A.scale_log2, v.y * A.scale_log2, v.z * A.scale_log2, v.w * A.scale_log2);
     }
     float m[4], l[4], o[4][4 * ND];
 #pragma unroll
@@ -78,32 +84,49 @@ __global__ void __launch_bounds__(kSimtThreads) shared_attn_simt_kernel(SharedAr
     for (int t = g.t0; t < g.t1; ++t) {
       const int np = min(kSharedTilePages, pages - t * kSharedTilePages);
       const int k0 = t * kSharedTile;
-      __syncthreads();
-      // stage the tile, row-major; what no row sees becomes zeros
-      constexpr int N = Vec16<T>::N, CH = kPageBlock * HD / N;
-      for (int e = tid; e < 2 * kSharedTilePages * CH; e += kSimtThreads) {
-        const int kv = e / (kSharedTilePages * CH), pg = e / CH % kSharedTilePages;
-        const int el = e % CH * N, tile = el / 64;
-        const int tok = tile / (HD / 8) * 8 + el % 64 / 8, d = tile % (HD / 8) * 8 + el % 8;
-        const int j = t * kSharedTilePages + pg, key = j * kPageBlock + tok;
-        Vec16<T> v;
-        v.raw = make_uint4(0, 0, 0, 0);
-        const bool seen = pg < np && (g.b < 0 || key < own_keys ||
-                                      (j >= n_own && key - n_own * kPageBlock < A.W));
-        if (seen) {
-          if (g.b >= 0 && j >= n_own) {
-            v = ld16(window_block<T>(A, g.b, j - n_own, kv, g.kvh, HD) + el);
-          } else {
-            const int id = own_page_id(A, g.b, sp.shared, j);
-            if (id >= 0 && id < A.num_pages)
-              v = ld16(cached_block<T>(A, id, kv, g.kvh, HD) + el);
-            else
-              set_err(A.err, WEDLM_DEV_BAD_PAGE);
-          }
+      // The tile's pages, then the tile, row-major: eight loads of a thread in flight
+      // at a time.  What no row sees becomes zeros.
+      if (tid < 2 * kSharedTilePages) {
+        const int kv = tid / kSharedTilePages, pg = tid % kSharedTilePages;
+        const int j = t * kSharedTilePages + pg;
+        const float* src = nullptr;
+        int seen = kPageBlock;  // tokens of the page that some row sees
+        if (pg >= np) {
+        } else if (g.b >= 0 && j >= n_own) {
+          src = window_block<float>(A, g.b, j - n_own, kv, g.kvh, HD);
+          seen = A.W - (j - n_own) * kPageBlock;
+        } else {
+          if (g.b >= 0) seen = own_keys - j * kPageBlock;
+          const int id = own_page_id(A, g.b, sp.shared, j);
+          if (id >= 0 && id < A.num_pages)
+            src = cached_block<float>(A, id, kv, g.kvh, HD);
+          else
+            set_err(A.err, WEDLM_DEV_BAD_PAGE);
         }
-        float* dst = (kv ? Vs : Ks) + (pg * kPageBlock + tok) * LD + d;
+        s_page[tid] = src;
+        s_seen[tid] = seen;
+      }
+      __syncthreads();  // also: the previous tile is done with
+      constexpr int CH = kPageBlock * HD / 4, NL = 2 * kSharedTilePages * CH / kSimtThreads;
+#pragma unroll 1
+      for (int i0 = 0; i0 < NL; i0 += 8) {
+        float4 v[8];
 #pragma unroll
-        for (int i = 0; i < N; ++i) dst[i] = v.get(i);
+        for (int i = 0; i < 8; ++i) {
+          const int e = tid + (i0 + i) * kSimtThreads, el = e % CH * 4;
+          const int tok = el / 64 / (HD / 8) * 8 + el % 64 / 8;
+          const float* src = s_page[e / CH];
+          v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (src && tok < s_seen[e / CH]) v[i] = *reinterpret_cast<const float4*>(src + el);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = tid + (i0 + i) * kSimtThreads, el = e % CH * 4, pg = e / CH;
+          const int tok = el / 64 / (HD / 8) * 8 + el % 64 / 8, d = el / 64 % (HD / 8) * 8 + el % 8;
+          float* dst = (pg >= kSharedTilePages ? Vs : Ks) +
+                       (pg % kSharedTilePages * kPageBlock + tok) * LD + d;
+          *reinterpret_cast<float4*>(dst) = v[i];
+        }
       }
       __syncthreads();
       float s[4][8];
@@ -287,13 +310,13 @@ __global__ void __launch_bounds__(2 * HD) shared_merge_kernel(const __grid_const
   }
 }
 
-template <typename T, int HD>
+template <int HD>
 cudaError_t launch_simt(const SharedArgs& A, cudaStream_t st) {
   constexpr int smem = simt_smem_bytes<HD>();
-  const cudaError_t e = cudaFuncSetAttribute(shared_attn_simt_kernel<T, HD>,
+  const cudaError_t e = cudaFuncSetAttribute(shared_attn_simt_kernel<HD>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(shared_attn_simt_kernel<T, HD>, dim3(A.grid), dim3(kSimtThreads), smem, st, A);
+  return launch_pdl(shared_attn_simt_kernel<HD>, dim3(A.grid), dim3(kSimtThreads), smem, st, A);
 }
 
 template <typename T, int HD>
@@ -310,7 +333,7 @@ cudaError_t launch_merge(const SharedArgs& A, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_shared_attention_simt(const SharedArgs& A, int hd, cudaStream_t st) {
-  return hd == 128 ? launch_simt<float, 128>(A, st) : launch_simt<float, 64>(A, st);
+  return hd == 128 ? launch_simt<128>(A, st) : launch_simt<64>(A, st);
 }
 
 cudaError_t launch_shared_merge(const SharedArgs& A, int hd, bool is_bf16, cudaStream_t st) {
