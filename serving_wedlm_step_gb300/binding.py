@@ -101,14 +101,6 @@ class SharedAttnArgs(ctypes.Structure):
         ("workspace_bytes", c_size_t), ("error", c_void_p)]
 
 
-class _Struct(c_void_p):
-    """A struct argument: packed bytes, a ctypes structure by reference, or None."""
-
-    @classmethod
-    def from_param(cls, x):
-        return ctypes.c_char_p(x) if isinstance(x, bytes) else x
-
-
 def load_library(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
@@ -141,10 +133,9 @@ def load_library(path: str = LIB_PATH):
                                   c_int32, POINTER(c_void_p), c_void_p, c_void_p]
     lib.wedlm_generate.argtypes = [c_void_p, POINTER(GenIn), c_void_p]
     lib.wedlm_dual_stream_attention.argtypes = [c_void_p, c_int32, c_int32] + [c_void_p] * 5
-    # structs as bytes, AppendArgs or SharedAttnArgs by reference, or None
-    lib.wedlm_append_kv.argtypes = [_Struct, c_void_p]
-    lib.wedlm_shared_attention.argtypes = [_Struct, c_void_p]
-    lib.wedlm_shared_attention_workspace.argtypes = [_Struct]
+    lib.wedlm_append_kv.argtypes = [POINTER(AppendArgs), c_void_p]
+    lib.wedlm_shared_attention.argtypes = [POINTER(SharedAttnArgs), c_void_p]
+    lib.wedlm_shared_attention_workspace.argtypes = [POINTER(SharedAttnArgs)]
     lib.wedlm_shared_attention_workspace.restype = c_size_t
     return lib
 
@@ -431,8 +422,23 @@ def _bad_arg(msg):
 # The two calls below take their structs as packed bytes: filling ctypes fields
 # one by one costs more than the kernels of a small call.  Field order and padding are
 # those of wedlm_append_args and wedlm_shared_attn_args (include/wedlm.h).
-_APPEND_PACK = struct.Struct("@8i2f" + "Pqqq" * 3 + "11P")
-_SHARED_PACK = struct.Struct("@9i4x8PNP")
+_APPEND_PACK = struct.Struct("@8i2f" + "Pqqq" * 3 + "11P").pack
+_SHARED_PACK = struct.Struct("@9i4x8PNP").pack
+_BYTES_FN = {}
+
+
+def _bytes_fn(name):
+    """The entry point `name`, its struct argument passed as bytes."""
+    fn = _BYTES_FN.get(name)
+    if fn is None:
+        fn = lib()[name]  # a function object of its own, with its own argument types
+        fn.argtypes = [ctypes.c_char_p] if name.endswith("_workspace") else \
+            [ctypes.c_char_p, c_void_p]
+        fn.restype = c_size_t if name.endswith("_workspace") else ctypes.c_int
+        _BYTES_FN[name] = fn
+    return fn
+
+
 _DTYPES = {}
 
 
@@ -519,7 +525,7 @@ def append_kv(k, v, pool, page_table, seq_len, counts=None, pos=None, q=None, q_
     if q is not None:
         nq = q.shape[2] if q.dim() == 4 else 0
         q_rows = _take_rows("q", q, dev, dt, B, n, nq, hd)
-    args = _APPEND_PACK.pack(
+    args = _APPEND_PACK(
         B, n, nq, nkv, hd, code, cols, _pool_pages(pool, nkv, hd), rms_eps, rope_theta,
         *_take_rows("k", k, dev, dt, B, n, nkv, hd), *_take_rows("v", v, dev, dt, B, n, nkv, hd),
         *q_rows, _take("q_norm", q_norm, dev, dt, (hd,)), _take("k_norm", k_norm, dev, dt, (hd,)),
@@ -529,7 +535,7 @@ def append_kv(k, v, pool, page_table, seq_len, counts=None, pos=None, q=None, q_
         _take("q_out", q_out, dev, dt, (B * n, nq, hd)),
         _take("kv_win", kv_win, dev, dt, (B, 2, nkv, (n + 15) // 16 * 16 * hd)),
         _take("new_seq_len", new_seq_len, dev, i32, (B,)), _take("error", error, dev, i32, (1,)))
-    rc = _on_device(dev, lib().wedlm_append_kv, args, _raw_stream(dev, stream))
+    rc = _on_device(dev, _bytes_fn("wedlm_append_kv"), args, _raw_stream(dev, stream))
     if rc != OK:
         raise WedlmError(rc, "wedlm_append_kv failed")
 
@@ -564,10 +570,9 @@ def shared_prefix_attention(q, pool, shared_pages, page_table, seq_len, kv_win, 
             _take("kv_win", kv_win, dev, dt, (B, 2, nkv, (W + 15) // 16 * 16 * hd)),
             _take("o", o, dev, dt, (M, nq * hd)))
     err = _take("error", error, dev, i32, (1,))
-    L = lib()
     if workspace is None:
-        need = L.wedlm_shared_attention_workspace(
-            _SHARED_PACK.pack(*sizes, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0))
+        need = _bytes_fn("wedlm_shared_attention_workspace")(
+            _SHARED_PACK(*sizes, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0))
         if need == 0:
             raise _bad_arg("sizes that wedlm_shared_attention does not take")
         if stream is None:
@@ -577,9 +582,9 @@ def shared_prefix_attention(q, pool, shared_pages, page_table, seq_len, kv_win, 
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise _bad_arg(f"workspace must be a contiguous tensor on cuda:{dev}")
-    args = _SHARED_PACK.pack(*sizes, *ptrs, workspace.data_ptr(),
+    args = _SHARED_PACK(*sizes, *ptrs, workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), err)
-    rc = _on_device(dev, L.wedlm_shared_attention, args, _raw_stream(dev, stream))
+    rc = _on_device(dev, _bytes_fn("wedlm_shared_attention"), args, _raw_stream(dev, stream))
     if rc != OK:
         raise WedlmError(rc, "wedlm_shared_attention failed")
     return o
@@ -592,7 +597,7 @@ def shared_prefix_workspace(batch, window, n_q_heads, n_kv_heads, head_dim, dtyp
     args = SharedAttnArgs(batch=batch, window=window, n_q_heads=n_q_heads, n_kv_heads=n_kv_heads,
                           head_dim=head_dim, dtype=dtype, n_shared_pages=n_shared_pages,
                           max_pages_per_seq=max_pages_per_seq, num_pages=1)
-    need = lib().wedlm_shared_attention_workspace(bytes(args))
+    need = lib().wedlm_shared_attention_workspace(ctypes.byref(args))
     if need == 0:
         raise _bad_arg("sizes that wedlm_shared_attention does not take")
     return need

@@ -2,6 +2,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "shared_attn.cuh"
 
@@ -9,6 +10,17 @@ namespace wedlm {
 namespace {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// SMs of the current device (asked once per device), 0 when there is none
+int device_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
 
 // Sizes of a call: its split and the workspace's layout.  False for sizes the
 // kernels do not take.
@@ -45,12 +57,13 @@ bool shared_plan(const wedlm_shared_attn_args& a, SharedPlan* P) {
   A.pblocks = (seq_rows + A.prows - 1) / A.prows;
   if (a.dtype == WEDLM_BF16) {
     // relative times, swept on GB300: a tile for 128 rows 16, for a pair of row
-    // blocks 20; a unit's start and end 24, more with the rows whose partial it
+    // blocks 28; a unit's start and end 32, more with the rows whose partial it
     // writes.  (All tiles alike, ends 12: 579 us for 64 sequences x 32 rows over
-    // 16384 shared positions, 405 us with these.)
-    A.ucost = 24 + std::min(A.prows, 128) / 8;
-    A.shared_cost = A.B * A.W > P->TPB ? 20 : 16;
-    A.private_cost = A.W > P->TPB ? 20 : 16;
+    // 16384 shared positions, 416 us with these; 64 single tokens over 8192 with
+    // pairs at 20: 47 us, 40 us with these.)
+    A.ucost = 32 + std::min(A.prows, 128) / 4;
+    A.shared_cost = A.B * A.W > P->TPB ? 28 : 16;
+    A.private_cost = A.W > P->TPB ? 28 : 16;
     A.min_share = 32;
   } else {
     A.ucost = 1;
@@ -104,10 +117,8 @@ extern "C" int wedlm_shared_attention(const wedlm_shared_attn_args* a, void* str
     return WEDLM_ERR_INVALID_ARG;
   if (a->workspace_bytes < P.bytes) return WEDLM_ERR_CAPACITY;
   SharedArgs& A = P.A;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return WEDLM_ERR_CUDA;
+  const int sms = device_sms();
+  if (sms < 1) return WEDLM_ERR_CUDA;
   A.grid = std::min(sms, kSharedMaxGrid);  // one block per SM
   A.q = a->q;
   A.pool = a->kv_pool;

@@ -313,8 +313,8 @@ __global__ void __launch_bounds__(2 * HD) shared_merge_kernel(const __grid_const
 template <int HD>
 cudaError_t launch_simt(const SharedArgs& A, cudaStream_t st) {
   constexpr int smem = simt_smem_bytes<HD>();
-  const cudaError_t e = cudaFuncSetAttribute(shared_attn_simt_kernel<HD>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = raise_smem(done, (const void*)shared_attn_simt_kernel<HD>, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(shared_attn_simt_kernel<HD>, dim3(A.grid), dim3(kSimtThreads), smem, st, A);
 }

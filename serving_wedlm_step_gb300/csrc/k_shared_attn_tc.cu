@@ -804,9 +804,8 @@ cudaError_t launch(const SharedArgs& A, int TPB, cudaStream_t st) {
     return cudaErrorInvalidValue;
   constexpr size_t kSmem = Cfg<HD>::kData + sizeof(Ctl<HD>);
   static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
-  const cudaError_t e = cudaFuncSetAttribute(shared_attn_tc_kernel<HD>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)kSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = raise_smem(done, (const void*)shared_attn_tc_kernel<HD>, (int)kSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(shared_attn_tc_kernel<HD>, dim3(A.grid), dim3(kThreads), kSmem, st, mq,
                     A, TPB);

@@ -17,9 +17,24 @@
 // The blocks that hold a unit's first and last tile record themselves, and
 // the merge walks the slots in between, in order.
 #pragma once
+#include <atomic>
+
 #include "internal.h"
 
 namespace wedlm {
+
+// Raise a kernel's dynamic shared-memory limit on the current device, once per
+// (kernel, device); throws nothing.  `done` is the kernel's own word.
+inline cudaError_t raise_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 constexpr int kSharedTile = 128;                            // keys per tile
 constexpr int kSharedTilePages = kSharedTile / kPageBlock;  // 8
