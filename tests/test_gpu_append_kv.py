@@ -202,6 +202,85 @@ def test_captured_and_replayed_on_new_rows():
     c.check(before)
 
 
+def test_on_another_stream():
+    """The call's stream is the one given: it waits there for what fills its rows."""
+    c = Case(4, 40, 8, 2, 128, BF, [0, 3, 16, 100], [40, 1, 0, 33], True, True, False, seed=12)
+    before = c.pool.clone()
+    rows = c.qkv.clone()
+    c.qkv.zero_()
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(2_000_000)
+        c.qkv.copy_(rows)
+    c.call(stream=st)
+    st.synchronize()
+    c.check(before)
+
+
+def test_rows_expanded_over_the_batch():
+    """One prompt for all sequences: rows with a batch stride of zero."""
+    c = Case(3, 5, 4, 2, 64, FP, [2, 17, 30], [5, 2, 4], True, True, False, seed=13)
+    before = c.pool.clone()
+    c.k, c.v, c.q = (t[:1].expand(3, -1, -1, -1) for t in (c.k, c.v, c.q))
+    c.call()
+    c.check(before)
+
+
+def test_binding_refuses_before_anything_is_enqueued():
+    from serving_wedlm_step_gb300 import binding as Bd
+    c = Case(2, 4, 4, 2, 64, FP, 0, [4, 4], True, True, False, seed=14)
+    before = c.pool.clone()
+    bad = [dict(counts=c.cnt.long()), dict(counts=c.cnt[:1]), dict(q=None), dict(q_out=None),
+           dict(q=c.q.to(BF)), dict(q_out=c.q_out[:, :, :32]), dict(kv_win=c.win[:1]),
+           dict(k_norm=c.kn.cpu()), dict(pos=torch.zeros(2, 3, dtype=torch.int32, device="cuda")),
+           dict(new_seq_len=c.seq_len), dict(error=torch.zeros(2, dtype=torch.int32).cuda()),
+           dict(rope_theta=0.0), dict(rms_eps=float("inf")), dict(q=c.qkv[:, :, :4, 1:])]
+    for kw in bad:
+        with pytest.raises(Bd.WedlmError) as e:
+            c.call(**kw)
+        assert e.value.code == Bd.ERR_INVALID_ARG, kw
+    k = c.k
+    for c.k in (k[:, :, :1], k[..., :48], k[:, :, :, 2:], k.half()):
+        with pytest.raises(Bd.WedlmError):
+            c.call()
+    torch.cuda.synchronize()
+    assert torch.equal(c.pool, before)
+
+
+def test_pages_are_there_for_the_window_attention_behind_it():
+    """wedlm_attention reads cached pages before it waits for the kernel in front
+    of it: straight behind an append it must still see the appended rows."""
+    from serving_wedlm_step_gb300 import binding as Bd
+    from synth import make_weights_torch, qwen3_layers
+    s = qwen3_layers(1).replace(vocab=256, ffn=128)
+    B, n, W = 4, 48, 16
+    c = Case(B, n, 0, 8, 128, BF, [0, 5, 16, 40], None, False, False, False, seed=15)
+    c.pool.zero_()
+    ctx = Bd.WedlmContext(s, make_weights_torch(s, seed=0), window=W, max_batch=B,
+                          max_pages_per_seq=c.table.shape[1])
+    table = c.table.clamp(min=0)
+    q = torch.randn(B * W, 32, 128, device="cuda").to(BF)
+    win = torch.randn(B, 2, 8, W * 128, device="cuda").to(BF)
+    outs = []
+    for i in range(8):
+        c.qkv[:, :, :-1].normal_()
+        o, ref = (torch.empty(B * W, 32 * 128, dtype=BF, device="cuda") for _ in range(2))
+        torch.cuda.synchronize()
+        c.call()
+        ctx.attention(q, c.pool, table, c.new_len, c.pool.shape[0], win, o)
+        torch.cuda.synchronize()
+        ctx.attention(q, c.pool, table, c.new_len, c.pool.shape[0], win, ref)
+        torch.cuda.synchronize()
+        assert ctx.status() == 0 and torch.equal(o, ref)
+        Bd.shared_prefix_attention(q, c.pool, None, table, c.new_len, win, ref)
+        # two bf16 results of one sum, each within 2^-8 of it for P and for the output
+        torch.testing.assert_close(o.float(), ref.float(), rtol=0, atol=4 * 2.0 ** -8)
+        outs.append(o)
+    assert not torch.equal(outs[0], outs[1])
+    ctx.close()
+
+
 def test_pool_beyond_32_bit_offsets():
     """Pages whose first value lies past 2^31 values and 2^32 bytes."""
     c = Case(2, 40, 0, 8, 128, BF, [0, 7], None, False, False, False, seed=2)

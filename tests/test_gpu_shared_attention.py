@@ -142,6 +142,38 @@ def test_bad_pages_and_lengths_are_reported():
     assert int(c.err) & Bd.DEV_BAD_PAGE and torch.isfinite(o).all()
 
 
+def test_binding_refuses_before_anything_is_enqueued():
+    from serving_wedlm_step_gb300 import binding as Bd
+    c = AttnCase([16 * 3 + 5, 16 * 3], 4, 4, 2, 64, 3, BF, seed=17)
+    o = c.out()
+
+    def refused(code=Bd.ERR_INVALID_ARG, **kw):
+        args = dict(q=c.q, pool=c.pool, shared_pages=c.shared, page_table=c.table,
+                    seq_len=c.seq_len, kv_win=c.win, o=o)
+        args.update(kw)
+        with pytest.raises(Bd.WedlmError) as e:
+            Bd.shared_prefix_attention(**args)
+        assert e.value.code == code, kw
+
+    refused(q=c.q.float())
+    refused(q=c.q[:, :3].contiguous())
+    refused(q=c.q[1:])
+    refused(q=c.q.transpose(0, 1).contiguous().transpose(0, 1))
+    refused(pool=c.pool[:, :, :, 1:])
+    refused(pool=c.pool.view(-1)[8:])
+    refused(shared_pages=c.shared.long())
+    refused(shared_pages=c.shared.cpu())
+    refused(page_table=c.table[:1])
+    refused(page_table=c.table[:, ::2])
+    refused(seq_len=c.seq_len.long())
+    refused(kv_win=c.win[:, :, :, 16:])
+    refused(o=o[:, :64])
+    refused(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"), code=Bd.ERR_CAPACITY)
+    refused(workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    torch.cuda.synchronize()
+    assert torch.isnan(o).all()
+
+
 def test_two_streams_at_once():
     """Calls that overlap, each with its own workspace."""
     a = AttnCase([16 * 80 + 100] * 8, 8, 8, 2, 128, 80, BF, seed=12)
