@@ -431,7 +431,7 @@ int wedlm_append_kv(const wedlm_append_args *args, void *stream);
 typedef struct wedlm_shared_attn_args {
   int32_t batch;               /* B, 1..1024                               */
   int32_t window;              /* W, 1..64 query rows per sequence         */
-  int32_t n_q_heads, n_kv_heads; /* G = n_q_heads / n_kv_heads, 1..128     */
+  int32_t n_q_heads, n_kv_heads; /* n_kv_heads 1..1024, their ratio G 1..128 */
   int32_t head_dim;            /* 64 or 128                                */
   int32_t dtype;               /* WEDLM_BF16 | WEDLM_FP32                  */
   int32_t n_shared_pages;      /* S >= 0 pages of shared prefix            */
