@@ -205,7 +205,7 @@ __device__ __forceinline__ void wait_st() {
 
 template <int HD> struct Ctl {
   uint64_t k_full[Cfg<HD>::kK], k_empty[Cfg<HD>::kK], v_full[Cfg<HD>::kV], v_empty[Cfg<HD>::kV];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t pair[4], fin;  // pair: the two softmax warps of a row
   Seg seg[kSegs];
@@ -263,7 +263,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       mbar_init(&ctl.q_empty[x], 2);
       mbar_init(&ctl.s_full[x], 1);
       mbar_init(&ctl.p_full[x], 8);
-      mbar_init(&ctl.pv_done[x], 1);
+      mbar_init(&ctl.o_done[x], 1);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
@@ -489,9 +489,9 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         vph ^= 1u;
       }
     };
-    // the tile whose P V is due: its number, pages, whether O starts with it, the
-    // ends of its cached keys and of the window in it
-    int pn = -1, pnp = 0, pfirst = 0, pc0 = 0, pc1 = 0;
+    // the tile whose P V is due: its number, pages, whether O starts or is complete
+    // with it, the ends of its cached keys and of the window in it
+    int pn = -1, pnp = 0, pfirst = 0, plast = 0, pc0 = 0, pc1 = 0;
     uint32_t pph = 0;
     bool have = get(g), ok = true;
 #pragma unroll 1
@@ -565,7 +565,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 #pragma unroll
           for (int k = 0; k < kSharedTilePages; ++k)  // 16 keys: 8 columns of P
             if (k < pnp) mma_ts(dO, dS + k * 8, dv + k * (HD * 2), idPV, (k || !pfirst) ? 1u : 0u);
-          tc_commit(&ctl.pv_done[x]);
+          if (plast) tc_commit(&ctl.o_done[x]);
           tc_commit(&ctl.v_empty[vst]);
         }
         if (tile) {
@@ -587,6 +587,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       pn = tile ? n : -1;
       pnp = np;
       pfirst = j == 0;
+      plast = j + 1 == (x ? g.nB : g.n);
       pc0 = g.b < 0 ? 0 : g.own_keys - t * kSharedTile;
       pc1 = g.b < 0 ? 0 : g.n_own * kPageBlock - t * kSharedTile + A.W;
     }
@@ -601,7 +602,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     const int r = 32 * q + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
     const float sc = A.scale_log2;
-    uint32_t sph = 0, dph = 0, jph = 0;  // phases: bit x of ctl.s_full and ctl.pv_done, of the pair's
+    uint32_t sph = 0, dph = 0, jph = 0;  // phases: bit x of s_full and o_done, of the pair's
     // The two warps of a row meet.  An mbarrier and not a named one, so that a wait
     // that expired elsewhere cannot leave one of them here for good.
     auto pair_sync = [&]() {
@@ -625,10 +626,6 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         float m = x ? m2[1] : m2[0];
         wait(&ctl.s_full[x], sph >> x & 1);
         sph ^= 1u << x;
-        // P V of the tile before is in O: done since S was, but every phase is seen
-        // (asked here, answered below, behind the loads of S)
-        const uint32_t pv_ph = (dph >> x & 1) ^ 1u;
-        const bool pv_ok = j == 0 || mbar_try_wait(&ctl.pv_done[x], pv_ph);
         tc_fence_after();
         // what this row does not see becomes -inf, in TMEM and in a rolled loop:
         // only a unit's last tiles need it
@@ -660,10 +657,6 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         float mt = max64(v) * sc;
         // Does a row of either warp raise its maximum?  The meeting also keeps P
         // from S columns the other warp has not read yet.
-        if (!__all_sync(0xffffffffu, pv_ok)) {
-          wait(&ctl.pv_done[x], pv_ph);
-          tc_fence_after();
-        }
         const int odd = ++tiles & 1;  // one of the two may be a tile ahead: two sets
         ctl.red[odd][h][r] = mt;
         if (__any_sync(0xffffffffu, mt > m + kRaise)) ctl.raise[odd][q] = tiles;
@@ -671,7 +664,7 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         if (ctl.raise[odd][q] == tiles) {
           mt = fmaxf(mt, ctl.red[odd][h ^ 1][r]);
           const bool raise = mt > m + kRaise;
-          if (j > 0) {
+          if (j > 0) {  // O holds the tiles before: S is committed behind their P V
             const float a = !raise ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - mt);
 #pragma unroll 1
             for (int c = 0; c < HD / 2; c += 16) {
@@ -694,12 +687,15 @@ shared_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.p_full[x]);
-        dph ^= 1u << x;
       }
       // The segment's partial: O once its last P V is done.  Pair: this warp's half
       // of the dims of both streams' rows.  Split: A and B joined.
-      wait(&ctl.pv_done[0], (dph & 1) ^ 1u);
-      if (g.nB > 0) wait(&ctl.pv_done[1], (dph >> 1) ^ 1u);
+      wait(&ctl.o_done[0], dph & 1);
+      dph ^= 1u;
+      if (g.nB > 0) {
+        wait(&ctl.o_done[1], dph >> 1);
+        dph ^= 2u;
+      }
       tc_fence_after();
       pair_sync();  // the other warp is done with `red` too
       ctl.red[h][0][r] = l2[0];  // the row sums are in halves

@@ -105,12 +105,21 @@ struct SharedWalk {
     const int per = (A.B + 31) / 32, b0 = min(A.B, lane * per), b1 = min(A.B, b0 + per);
     int sum = 0, any = 0;
 #pragma unroll 1
-    for (int i = b0; i < b1; ++i) {
-      if (blockIdx.x == 0) check_len(A, i);
-      const SeqSpan s = seq_span(A, i);
-      any |= s.shared;
-      sum += units * (A.ucost + own_tiles(A, s) * A.private_cost);
+    for (int i = b0; i < b1; i += 4) {
+      SeqSpan s[4];  // four loads in flight
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] = seq_span(A, min(i + k, b1 - 1));
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k < b1) {
+          any |= s[k].shared;
+          sum += A.ucost + own_tiles(A, s[k]) * A.private_cost;
+        }
     }
+    sum *= units;
+    if (blockIdx.x == 0)
+#pragma unroll 1
+      for (int i = b0; i < b1; ++i) check_len(A, i);
     any = __any_sync(0xffffffffu, any);
     int incl = sum;
 #pragma unroll 1
