@@ -58,9 +58,10 @@ bool shared_plan(const wedlm_shared_attn_args& a, SharedPlan* P) {
   if (a.dtype == WEDLM_BF16) {
     // relative times, swept on GB300: a tile for 128 rows 16, for a pair of row
     // blocks 28; a unit's start and end 32, more with the rows whose partial it
-    // writes.  (All tiles alike, ends 12: 579 us for 64 sequences x 32 rows over
-    // 16384 shared positions, 416 us with these; 64 single tokens over 8192 with
-    // pairs at 20: 47 us, 40 us with these.)
+    // writes.  (When this was first swept, all tiles alike and ends 12 took 579 us
+    // for 64 sequences x 32 rows over 16384 shared positions, these 416; 64 single
+    // tokens over 8192 with pairs at 20 took 47 us, with these 40.  Today 400 and
+    // 39, pairs at 24 to 32 or ends at 24 to 48 within 2 % and 14 % of them.)
     A.ucost = 32 + std::min(A.prows, 128) / 4;
     A.shared_cost = A.B * A.W > P->TPB ? 28 : 16;
     A.private_cost = A.W > P->TPB ? 28 : 16;
