@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(2 * HD) shared_merge_kernel(const __grid_const
     float4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = src[(size_t)k * st];
-    if (ml.x == -INFINITY) continue;  // no key seen: its O is not even written
+    if (ml.y == 0.f) continue;  // no key seen (keys that are all NaN leave l NaN)
     const float w = exp2f(ml.x - M);
     l = fmaf(ml.y, w, l);
 #pragma unroll

@@ -33,6 +33,20 @@ def test_matches_formula(dtype, S, own, W, nq, nkv, hd):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("S,own,W", [(3, [0, 0], 1), (40, [0, 300], 1), (9, [0, 20], 40)])
+def test_a_visible_nan_is_not_lost_with_its_range(dtype, S, own, W):
+    """The one key of its own that a row sees is NaN, the shared ones are finite: the
+    row is NaN, the other sequences are what they were."""
+    c = AttnCase([PAGE * S + n for n in own], W, 8, 2, 128, S, dtype, seed=S)
+    before = c.call()
+    c.win[0, 0, 1, :8] = float("nan")  # 8 dims of K of the first window row, kv head 1
+    o = c.call().view(len(own), W, 8, 128)
+    assert o[0, :, 4:].isnan().all()
+    old = before.view(len(own), W, 8, 128)
+    assert torch.equal(o[0, :, :4], old[0, :, :4]) and torch.equal(o[1:], old[1:])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("W,lens", [
     (1, [0, 160, 159, 1, 500, 0]),    # padded slots and sequences shorter than the prefix
     (16, [0, 0, 0]),                  # nobody takes part
