@@ -399,8 +399,9 @@ typedef struct wedlm_append_args {
   void *q_out;                 /* [B*n][n_q_heads][head_dim]; with q only  */
   void *kv_win;                /* [B][2][n_kv_heads][Wp][head_dim] in the page
                                   tile layout (Wp = n rounded up to 16), or NULL */
-  int32_t *new_seq_len;        /* [B] seq_len + appended rows, or NULL; not
-                                  the same memory as seq_len               */
+  int32_t *new_seq_len;        /* [B] seq_len + appended rows, or NULL; in
+                                  none of the memory of seq_len, counts, pos
+                                  and page_table                           */
   int32_t *error;              /* device word that WEDLM_DEV_* bits are OR-ed
                                   into, or NULL; never cleared here        */
 } wedlm_append_args;

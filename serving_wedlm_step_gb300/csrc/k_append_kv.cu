@@ -242,13 +242,22 @@ extern "C" int wedlm_append_kv(const wedlm_append_args* a, void* stream) {
       !a->kv_pool || bad16(a->kv_pool) || bad16(a->kv_win) || bad16(a->q_out) ||
       bad16(a->q_norm) || bad16(a->k_norm) || bad4(a->pos) || bad4(a->counts) ||
       bad4(a->seq_len) || bad4(a->page_table) || bad4(a->new_seq_len) || bad4(a->error) ||
-      (a->kv_win && a->rows > kMaxWindow) || (a->new_seq_len && a->new_seq_len == a->seq_len))
+      (a->kv_win && a->rows > kMaxWindow))
     return WEDLM_ERR_INVALID_ARG;
   const int es = a->dtype == WEDLM_BF16 ? 2 : 4;
   const bool has_q = a->q.ptr != nullptr;
   if (bad_rows(a->k, es) || bad_rows(a->v, es) || has_q != (a->q_out != nullptr) ||
       (!has_q && a->q_norm) ||
       (has_q && (bad_rows(a->q, es) || a->n_q_heads < 1 || a->n_q_heads > 8192)))
+    return WEDLM_ERR_INVALID_ARG;
+  // one block writes new_seq_len while the others still read
+  auto meets = [&](const int32_t* p, int64_t n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a->new_seq_len), y = reinterpret_cast<uintptr_t>(p);
+    return x && y && x < y + 4 * (uintptr_t)n && y < x + 4 * (uintptr_t)a->batch;
+  };
+  if (meets(a->seq_len, a->batch) || meets(a->counts, a->batch) ||
+      meets(a->pos, (int64_t)a->batch * a->rows) ||
+      meets(a->page_table, (int64_t)a->batch * a->max_pages_per_seq))
     return WEDLM_ERR_INVALID_ARG;
   AppendArgs A;
   A.B = a->batch;

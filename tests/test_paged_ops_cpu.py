@@ -48,6 +48,15 @@ def test_append_refuses(Bd, bad):
     assert Bd.lib().wedlm_append_kv(ctypes.byref(args), None) == Bd.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("bad", [
+    dict(seq_len=2 * P + 4), dict(seq_len=2 * P - 4), dict(counts=2 * P), dict(counts=2 * P + 4),
+    dict(pos=2 * P - 4 * 15), dict(page_table=2 * P - 4 * 7),
+])
+def test_append_refuses_new_lengths_over_what_is_still_read(Bd, bad):
+    args = append_args(Bd, **bad)  # batch 2, 8 rows, 4 pages a sequence
+    assert Bd.lib().wedlm_append_kv(ctypes.byref(args), None) == Bd.ERR_INVALID_ARG
+
+
 def attn_args(Bd, **kw):
     base = dict(batch=2, window=8, n_q_heads=8, n_kv_heads=2, head_dim=128, dtype=Bd.BF16,
                 n_shared_pages=3, max_pages_per_seq=6, num_pages=9, q=P, kv_pool=P,
