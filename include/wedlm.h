@@ -423,8 +423,9 @@ typedef struct wedlm_append_args {
  * negative seq_len, or a count outside 0..n, sets WEDLM_DEV_BAD_SEQLEN; the
  * former appends nothing (and its rows without `pos` rotate as if it were 0),
  * the latter is clamped.  new_seq_len stops at the page table's capacity.
- * No two appended rows may go to one place of the pool.  No context, workspace
- * or allocation; calls on different streams are independent.  Returns
+ * No two appended rows may go to one place of the pool, and no output may
+ * overlap an input (for new_seq_len this is checked).  No context, workspace or
+ * allocation; calls on different streams are independent.  Returns
  * WEDLM_ERR_INVALID_ARG (nothing enqueued) or WEDLM_ERR_CUDA. */
 int wedlm_append_kv(const wedlm_append_args *args, void *stream);
 
@@ -475,7 +476,8 @@ size_t wedlm_shared_attention_workspace(const wedlm_shared_attn_args *args);
  *    calls that may overlap on the GPU (two streams, two captured graphs)
  *    need one each.  No context and no allocation.  The result is the same,
  *    bit for bit, whenever the inputs are.
- *  - q, kv_pool, kv_win and o are 16-byte aligned and contiguous.
+ *  - q, kv_pool, kv_win and o are 16-byte aligned and contiguous; o and the
+ *    workspace overlap no input and not each other.
  *  - Limit: n_kv_heads * (row blocks of the batch * S/8 + B * row blocks of a
  *    window * max_pages_per_seq/8) stays below 2^31 (a row block: 128 rows or
  *    more in bf16, 64 in fp32, of the G rows per token).
