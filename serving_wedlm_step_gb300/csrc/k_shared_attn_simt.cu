@@ -260,35 +260,47 @@ __global__ void __launch_bounds__(2 * HD) shared_merge_kernel(const __grid_const
   const float2* ml_p = A.ml_p + (size_t)seg_slot(A, up, bp.x) * A.prows + ip;
   const float4* o_s = A.part_s + ((size_t)seg_slot(A, us, bs.x) * (HD / 4) + d40) * A.srows + is;
   const float4* o_p = A.part_p + ((size_t)seg_slot(A, up, bp.x) * (HD / 4) + d40) * A.prows + ip;
-  // the row's maximum
-  float M = -INFINITY;
+  // partial i of the row
+  auto fetch = [&](int i, float2& ml, float4 (&v)[4]) {
+    const bool sh = i < ns;
+    const int st = sh ? A.srows : A.prows, q = sh ? i : i - ns;
+    const float4* src = (sh ? o_s : o_p) + (size_t)q * (HD / 4) * st;
+    ml = (sh ? ml_s : ml_p)[(size_t)q * st];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = src[(size_t)k * st];
+  };
+  // the row's maximum; the first partial comes meanwhile, and then one ahead
+  float2 ml = make_float2(-INFINITY, 0.f);
+  float4 v[4] = {};
+  if (grp < n) fetch(grp, ml, v);
+  float M = ml.x;
 #pragma unroll 4
-  for (int i = grp; i < n; i += NG)
+  for (int i = grp + NG; i < n; i += NG)
     M = fmaxf(M, (i < ns ? ml_s[(size_t)i * A.srows] : ml_p[(size_t)(i - ns) * A.prows]).x);
 #pragma unroll
   for (int o = RPB; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float l = 0.f, acc[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-#pragma unroll 2
+#pragma unroll 1
   for (int i = grp; i < n; i += NG) {
-    const bool sh = i < ns;
-    const int st = sh ? A.srows : A.prows, q = sh ? i : i - ns;
-    const float2 ml = (sh ? ml_s : ml_p)[(size_t)q * st];
-    const float4* src = (sh ? o_s : o_p) + (size_t)q * (HD / 4) * st;
-    float4 v[4];
+    float2 ml_next = ml;
+    float4 next[4] = {};
+    if (i + NG < n) fetch(i + NG, ml_next, next);
+    if (ml.y != 0.f) {  // else no key seen (keys that are all NaN leave l NaN)
+      const float w = exp2f(ml.x - M);
+      l = fmaf(ml.y, w, l);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = src[(size_t)k * st];
-    if (ml.y == 0.f) continue;  // no key seen (keys that are all NaN leave l NaN)
-    const float w = exp2f(ml.x - M);
-    l = fmaf(ml.y, w, l);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      acc[4 * k] = fmaf(v[k].x, w, acc[4 * k]);
-      acc[4 * k + 1] = fmaf(v[k].y, w, acc[4 * k + 1]);
-      acc[4 * k + 2] = fmaf(v[k].z, w, acc[4 * k + 2]);
-      acc[4 * k + 3] = fmaf(v[k].w, w, acc[4 * k + 3]);
+      for (int k = 0; k < 4; ++k) {
+        acc[4 * k] = fmaf(v[k].x, w, acc[4 * k]);
+        acc[4 * k + 1] = fmaf(v[k].y, w, acc[4 * k + 1]);
+        acc[4 * k + 2] = fmaf(v[k].z, w, acc[4 * k + 2]);
+        acc[4 * k + 3] = fmaf(v[k].w, w, acc[4 * k + 3]);
+      }
     }
+    ml = ml_next;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = next[k];
   }
 #pragma unroll
   for (int o = RPB; o < 32; o <<= 1) {
