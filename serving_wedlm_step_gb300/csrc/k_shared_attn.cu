@@ -60,15 +60,20 @@ bool shared_plan(const wedlm_shared_attn_args& a, SharedPlan* P) {
     // blocks 28; a unit's start and end 32, more with the rows whose partial it
     // writes.  (When this was first swept, all tiles alike and ends 12 took 579 us
     // for 64 sequences x 32 rows over 16384 shared positions, these 416; 64 single
-    // tokens over 8192 with pairs at 20 took 47 us, with these 40.  Today 400 and
+    // tokens over 8192 with pairs at 20 took 47 us, with these 40.  Later 400 and
     // 39, pairs at 24 to 32 or ends at 24 to 48 within 2 % and 14 % of them.)
     A.ucost = 32 + std::min(A.prows, 128) / 4;
     A.shared_cost = A.B * A.W > P->TPB ? 28 : 16;
     A.private_cost = A.W > P->TPB ? 28 : 16;
     A.min_share = 32;
   } else {
-    A.ucost = 1;
-    A.shared_cost = A.private_cost = A.min_share = 1;
+    // a tile of 64 rows 4, of 16 rows 2, a unit's ends 2 (swept with a slower merge:
+    // 12 sequences x 8 rows over 2048 shared positions 23.4 us, 24.5 with 16 rows at
+    // 3, 28.5 with all at 1)
+    A.ucost = 2;
+    A.shared_cost = A.srows > kSimtFewRows ? 4 : 2;
+    A.private_cost = A.prows > kSimtFewRows ? 4 : 2;
+    A.min_share = std::max(A.shared_cost, A.private_cost);
   }
   // the split counts in 31 bits: where full tables could pass that, a tile and a
   // unit's ends weigh 1, and beyond that the call is refused

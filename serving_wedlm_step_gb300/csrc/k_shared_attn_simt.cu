@@ -6,9 +6,17 @@
 //   s = q k * log2(e)/sqrt(hd),  m' = max(m, max s),
 //   l = l 2^(m-m') + sum 2^(s-m'),  O = O 2^(m-m') + 2^(s-m') V
 // 64 rows x 128 keys per tile, 256 threads; a thread owns 4 rows x 8 keys of S
-// and 4 rows x 8 (4) dims of O, so a step of 4 dims (keys) does 128 FMAs on
-// 12 shared-memory vectors.  K, V and Q rows are padded by 4 floats: 8 lanes
-// that read 8 rows touch 32 different banks.
+// and 4 rows x 8 (4) dims of O, so a step of 4 dims (keys) does 128 FMAs, in
+// pairs, on 12 shared-memory vectors.  K, V and Q rows are padded by 4 floats: 8
+// lanes that read 8 rows touch 32 different banks.  V comes during S, the next K
+// during P V.  What bounds it is the latency of the shared-memory reads, with two
+// warps a scheduler: 40 sequences x 32 rows of 4 heads of 128 over 8192 shared
+// positions 590 us, 37 TFLOP/s (FMAs one by one 618 us).
+//
+// Units of at most 16 rows (a window's own keys, most often) take tiles of 16 rows,
+// one a thread: 12 sequences x 8 rows of 4 heads of 64 over 2048 shared positions
+// take 21 us so, 27 us with 64-row tiles for all; a single row over 32768 takes 35
+// and 47 us.
 #include "shared_attn.cuh"
 
 namespace wedlm {
@@ -17,34 +25,273 @@ namespace {
 constexpr int kSimtThreads = 256;
 constexpr int kPRow = kSharedTile + 4;
 
+__device__ __forceinline__ void cp_async16(float* dst, const float* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all groups but the newest are there
+__device__ __forceinline__ void cp_wait_but_last() {
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+
 template <int HD> constexpr int simt_smem_bytes() {
   return ((kSimtRows + 2 * kSharedTile) * (HD + 4) + kSimtRows * kPRow) * (int)sizeof(float);
+}
+
+// where a tile's pages lie (null: zeros), and the tokens of each that some row
+// sees: of K, then of V
+struct SimtPages {
+  const float* src[2 * kSharedTilePages];
+  int seen[2 * kSharedTilePages];
+};
+
+// One segment of a unit of up to 16 * RPT rows; thread (tx, ty) owns rows
+// ty * RPT .. and keys tx + 16 j.
+template <int HD, int RPT>
+__device__ __forceinline__ void simt_segment(const SharedArgs& A, const SharedSeg& g, float* sm,
+                                             SimtPages* s_pages) {
+  constexpr int LD = HD + 4, ND = HD / 64;
+  float* Qs = sm;                        // [64][LD], scaled
+  float* Ks = Qs + kSimtRows * LD;       // [128][LD]
+  float* Vs = Ks + kSharedTile * LD;     // [128][LD]
+  float* Ps = Vs + kSharedTile * LD;     // [64][kPRow]
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int nq = A.nkv * A.G;
+  const SeqSpan sp = g.sp;
+  const int n_own = g.b < 0 ? 0 : own_pages(sp);
+  const int own_keys = sp.len - sp.shared * kPageBlock;
+  const int pages = g.b < 0 ? A.nsp : n_own + A.Wp / kPageBlock;
+  const int urows = g.b < 0 ? A.srows : A.prows;
+  const int all_rows = (g.b < 0 ? A.B : 1) * A.W * A.G;
+  const int row0 = g.blk * urows, nrows = min(urows, all_rows - row0);
+  const int tok0 = g.b < 0 ? 0 : g.b * A.W;
+  // A tile's pages: their ids a phase ahead, then the addresses, which the copies of
+  // the phase after find in shared memory
+  auto id_of = [&](int t) -> int {
+    const int j = t * kSharedTilePages + tid % kSharedTilePages;
+    return tid < 2 * kSharedTilePages && t < g.t1 && j < (g.b < 0 ? pages : n_own)
+               ? own_page_id(A, g.b, sp.shared, j)
+               : -1;
+  };
+  auto put_pages = [&](int t, int id) {
+    if (tid >= 2 * kSharedTilePages || t >= g.t1) return;
+    const int kv = tid / kSharedTilePages, j = t * kSharedTilePages + tid % kSharedTilePages;
+    const float* src = nullptr;
+    int seen = kPageBlock;
+    if (j >= pages) {
+    } else if (g.b >= 0 && j >= n_own) {
+      src = window_block<float>(A, g.b, j - n_own, kv, g.kvh, HD);
+      seen = A.W - (j - n_own) * kPageBlock;
+    } else {
+      if (g.b >= 0) seen = own_keys - j * kPageBlock;
+      if (id >= 0 && id < A.num_pages)
+        src = cached_block<float>(A, id, kv, g.kvh, HD);
+      else
+        set_err(A.err, WEDLM_DEV_BAD_PAGE);
+    }
+    s_pages[t & 1].src[tid] = src;
+    s_pages[t & 1].seen[tid] = seen;
+  };
+  // K or V of a tile, row-major; what no row sees becomes zeros
+  auto copy = [&](int t, int kv) {
+    constexpr int CH = kPageBlock * HD / 4;
+    const SimtPages& pg = s_pages[t & 1];
+#pragma unroll
+    for (int i = 0; i < kSharedTilePages * CH / kSimtThreads; ++i) {
+      const int e = tid + i * kSimtThreads, j = e / CH, el = e % CH * 4;
+      const int tok = el / 64 / (HD / 8) * 8 + el % 64 / 8, d = el / 64 % (HD / 8) * 8 + el % 8;
+      const float* src = pg.src[kv * kSharedTilePages + j];
+      float* dst = (kv ? Vs : Ks) + (j * kPageBlock + tok) * LD + d;
+      if (src && tok < pg.seen[kv * kSharedTilePages + j])
+        cp_async16(dst, src + el);
+      else
+        *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  const int first_id = id_of(g.t0);
+  const float* q = static_cast<const float*>(A.q);
+#pragma unroll
+  for (int i = 0; i < 16 * RPT * HD / 4 / kSimtThreads; ++i) {
+    const int e = tid + i * kSimtThreads, r = e / (HD / 4), d = e % (HD / 4) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < nrows) {
+      const int row = row0 + r;
+      v = *reinterpret_cast<const float4*>(
+          q + ((size_t)(tok0 + row / A.G) * nq + g.kvh * A.G + row % A.G) * HD + d);
+    }
+    *reinterpret_cast<float4*>(Qs + r * LD + d) = make_float4(
+        v.x * A.scale_log2, v.y * A.scale_log2, v.z * A.scale_log2, v.w * A.scale_log2);
+  }
+  float m[RPT], l[RPT];
+  uint64_t o[RPT][2 * ND];  // pairs of dims
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2 * ND; ++j) o[i][j] = 0;
+  }
+  put_pages(g.t0, first_id);
+  __syncthreads();
+  copy(g.t0, 0);
+  cp_commit();
+  for (int t = g.t0; t < g.t1; ++t) {
+    const int np = min(kSharedTilePages, pages - t * kSharedTilePages);
+    const int k0 = t * kSharedTile, next_id = id_of(t + 1);
+    copy(t, 1);  // on its way during S, as the next K is during P V
+    cp_commit();
+    cp_wait_but_last();
+    __syncthreads();  // K (and Q) are there
+    uint64_t s2[RPT][8];  // even and odd dims
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s2[i][j] = 0;
+#pragma unroll 2
+    for (int d = 0; d < HD; d += 4) {
+      ulonglong2 qv[RPT], kv2[8];
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+        qv[i] = *reinterpret_cast<const ulonglong2*>(Qs + (ty * RPT + i) * LD + d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        kv2[j] = *reinterpret_cast<const ulonglong2*>(Ks + (tx + 16 * j) * LD + d);
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s2[i][j] = fma2(qv[i].x, kv2[j].x, s2[i][j]);
+          s2[i][j] = fma2(qv[i].y, kv2[j].y, s2[i][j]);
+        }
+    }
+    float s[RPT][8];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 e = unpack2(s2[i][j]);
+        s[i][j] = e.x + e.y;
+      }
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int p_row = (row0 + ty * RPT + i) / A.G;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int key = k0 + tx + 16 * j;
+        bool ok = tx + 16 * j < np * kPageBlock;
+        if (g.b >= 0) {
+          const int w = key - n_own * kPageBlock;
+          ok = ok && (w < 0 ? key < own_keys : w < A.W && w <= p_row);
+        }
+        if (!ok) s[i][j] = -INFINITY;
+        mx = fmaxf(mx, s[i][j]);
+      }
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1)
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const float mn = fmaxf(m[i], mx);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float a = exp2f(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p = exp2f(s[i][j] - base);
+        sum += p;
+        Ps[(ty * RPT + i) * kPRow + tx + 16 * j] = p;
+      }
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      l[i] = l[i] * a + sum;
+      m[i] = mn;
+#pragma unroll
+      for (int j = 0; j < 2 * ND; ++j) o[i][j] = mul2(o[i][j], pack2(a, a));
+    }
+    put_pages(t + 1, next_id);
+    __syncthreads();  // K has been read; P and the next tile's pages are there
+    if (t + 1 < g.t1) copy(t + 1, 0);
+    cp_commit();
+    cp_wait_but_last();
+    __syncthreads();  // V is there
+#pragma unroll 2
+    for (int k = 0; k < np * kPageBlock; k += 4) {
+      float4 pv[RPT];
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+        pv[i] = *reinterpret_cast<const float4*>(Ps + (ty * RPT + i) * kPRow + k);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int j = 0; j < ND; ++j) {
+          const ulonglong2 v =
+              *reinterpret_cast<const ulonglong2*>(Vs + (k + kk) * LD + tx * 4 + 64 * j);
+#pragma unroll
+          for (int i = 0; i < RPT; ++i) {
+            const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
+            o[i][2 * j] = fma2(pack2(p, p), v.x, o[i][2 * j]);
+            o[i][2 * j + 1] = fma2(pack2(p, p), v.y, o[i][2 * j + 1]);
+          }
+        }
+    }
+    __syncthreads();  // V and P have been read
+  }
+  if (tid == 0) record_unit(A, g);
+  const size_t slot = seg_slot(A, g.unit, blockIdx.x);
+  float4* po = (g.b < 0 ? A.part_s : A.part_p) + slot * urows * (HD / 4);
+  float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + slot * urows;
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = ty * RPT + i;
+    if (r >= nrows) continue;
+#pragma unroll
+    for (int j = 0; j < ND; ++j)
+    {
+      const float2 x = unpack2(o[i][2 * j]), y = unpack2(o[i][2 * j + 1]);
+      po[(size_t)(tx + 16 * j) * urows + r] = make_float4(x.x, x.y, y.x, y.y);
+    }
+    if (tx == 0) ml[r] = make_float2(m[i], l[i]);
+  }
 }
 
 template <int HD>
 __global__ void __launch_bounds__(kSimtThreads)
 shared_attn_simt_kernel(const __grid_constant__ SharedArgs A) {
-  constexpr int LD = HD + 4, ND = HD / 64;
   extern __shared__ __align__(16) float sm[];
-  float* Qs = sm;                        // [64][LD], scaled
-  float* Ks = Qs + kSimtRows * LD;       // [128][LD]
-  float* Vs = Ks + kSharedTile * LD;     // [128][LD]
-  float* Ps = Vs + kSharedTile * LD;     // [64][kPRow]
   __shared__ SharedSeg s_seg;
   __shared__ bool s_more;
-  __shared__ const float* s_page[2 * kSharedTilePages];
-  __shared__ int s_seen[2 * kSharedTilePages];
+  __shared__ SimtPages s_pages[2];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int nq = A.nkv * A.G;
   SharedWalk walk;
-  if (tid < 32) walk.init(A);
+  if (threadIdx.x < 32) walk.init(A);
   while (true) {
-    if (tid < 32) {
+    if (threadIdx.x < 32) {
       SharedSeg next;
       const bool more = walk.next(A, next);
-      if (tid == 0) {
+      if (threadIdx.x == 0) {
         s_seg = next;
         s_more = more;
       }
@@ -52,180 +299,10 @@ shared_attn_simt_kernel(const __grid_constant__ SharedArgs A) {
     __syncthreads();  // also: the previous segment is done with shared memory
     if (!s_more) break;
     const SharedSeg g = s_seg;
-    const SeqSpan sp = g.sp;
-    const int n_own = g.b < 0 ? 0 : own_pages(sp);
-    const int own_keys = sp.len - sp.shared * kPageBlock;
-    const int pages = g.b < 0 ? A.nsp : n_own + A.Wp / kPageBlock;
-    const int urows = g.b < 0 ? A.srows : A.prows;
-    const int all_rows = (g.b < 0 ? A.B : 1) * A.W * A.G;
-    const int row0 = g.blk * urows, nrows = min(urows, all_rows - row0);
-    const int tok0 = g.b < 0 ? 0 : g.b * A.W;
-    const float* q = static_cast<const float*>(A.q);
-#pragma unroll
-    for (int i = 0; i < kSimtRows * HD / 4 / kSimtThreads; ++i) {
-      const int e = tid + i * kSimtThreads, r = e / (HD / 4), d = e % (HD / 4) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < nrows) {
-        const int row = row0 + r;
-        v = *reinterpret_cast<const float4*>(
-            q + ((size_t)(tok0 + row / A.G) * nq + g.kvh * A.G + row % A.G) * HD + d);
-      }
-      *reinterpret_cast<float4*>(Qs + r * LD + d) = make_float4(
-          v.x * A.scale_log2, v.y * A.scale_log2, v.z * A.scale_log2, v.w * A.scale_log2);
-    }
-    float m[4], l[4], o[4][4 * ND];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4 * ND; ++j) o[i][j] = 0.f;
-    }
-    for (int t = g.t0; t < g.t1; ++t) {
-      const int np = min(kSharedTilePages, pages - t * kSharedTilePages);
-      const int k0 = t * kSharedTile;
-      // The tile's pages, then the tile, row-major: eight loads of a thread in flight
-      // at a time.  What no row sees becomes zeros.
-      if (tid < 2 * kSharedTilePages) {
-        const int kv = tid / kSharedTilePages, pg = tid % kSharedTilePages;
-        const int j = t * kSharedTilePages + pg;
-        const float* src = nullptr;
-        int seen = kPageBlock;  // tokens of the page that some row sees
-        if (pg >= np) {
-        } else if (g.b >= 0 && j >= n_own) {
-          src = window_block<float>(A, g.b, j - n_own, kv, g.kvh, HD);
-          seen = A.W - (j - n_own) * kPageBlock;
-        } else {
-          if (g.b >= 0) seen = own_keys - j * kPageBlock;
-          const int id = own_page_id(A, g.b, sp.shared, j);
-          if (id >= 0 && id < A.num_pages)
-            src = cached_block<float>(A, id, kv, g.kvh, HD);
-          else
-            set_err(A.err, WEDLM_DEV_BAD_PAGE);
-        }
-        s_page[tid] = src;
-        s_seen[tid] = seen;
-      }
-      __syncthreads();  // also: the previous tile is done with
-      constexpr int CH = kPageBlock * HD / 4, NL = 2 * kSharedTilePages * CH / kSimtThreads;
-#pragma unroll 1
-      for (int i0 = 0; i0 < NL; i0 += 8) {
-        float4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = tid + (i0 + i) * kSimtThreads, el = e % CH * 4;
-          const int tok = el / 64 / (HD / 8) * 8 + el % 64 / 8;
-          const float* src = s_page[e / CH];
-          v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (src && tok < s_seen[e / CH]) v[i] = *reinterpret_cast<const float4*>(src + el);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = tid + (i0 + i) * kSimtThreads, el = e % CH * 4, pg = e / CH;
-          const int tok = el / 64 / (HD / 8) * 8 + el % 64 / 8, d = el / 64 % (HD / 8) * 8 + el % 8;
-          float* dst = (pg >= kSharedTilePages ? Vs : Ks) +
-                       (pg % kSharedTilePages * kPageBlock + tok) * LD + d;
-          *reinterpret_cast<float4*>(dst) = v[i];
-        }
-      }
-      __syncthreads();
-      float s[4][8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[i][j] = 0.f;
-#pragma unroll 2
-      for (int d = 0; d < HD; d += 4) {
-        float4 qv[4], kv4[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          qv[i] = *reinterpret_cast<const float4*>(Qs + (ty * 4 + i) * LD + d);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          kv4[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * LD + d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            s[i][j] = fmaf(qv[i].x, kv4[j].x, s[i][j]);
-            s[i][j] = fmaf(qv[i].y, kv4[j].y, s[i][j]);
-            s[i][j] = fmaf(qv[i].z, kv4[j].z, s[i][j]);
-            s[i][j] = fmaf(qv[i].w, kv4[j].w, s[i][j]);
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int p_row = (row0 + ty * 4 + i) / A.G;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int key = k0 + tx + 16 * j;
-          bool ok = tx + 16 * j < np * kPageBlock;
-          if (g.b >= 0) {
-            const int w = key - n_own * kPageBlock;
-            ok = ok && (w < 0 ? key < own_keys : w < A.W && w <= p_row);
-          }
-          if (!ok) s[i][j] = -INFINITY;
-          mx = fmaxf(mx, s[i][j]);
-        }
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1)
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const float mn = fmaxf(m[i], mx);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float a = exp2f(m[i] - base);
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float p = exp2f(s[i][j] - base);
-          sum += p;
-          Ps[(ty * 4 + i) * kPRow + tx + 16 * j] = p;
-        }
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        l[i] = l[i] * a + sum;
-        m[i] = mn;
-#pragma unroll
-        for (int j = 0; j < 4 * ND; ++j) o[i][j] *= a;
-      }
-      __syncwarp();  // a row's P is written and read by the same warp
-#pragma unroll 2
-      for (int k = 0; k < np * kPageBlock; k += 4) {
-        float4 pv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          pv[i] = *reinterpret_cast<const float4*>(Ps + (ty * 4 + i) * kPRow + k);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int j = 0; j < ND; ++j) {
-            const float4 v = *reinterpret_cast<const float4*>(Vs + (k + kk) * LD + tx * 4 + 64 * j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
-              o[i][4 * j] = fmaf(p, v.x, o[i][4 * j]);
-              o[i][4 * j + 1] = fmaf(p, v.y, o[i][4 * j + 1]);
-              o[i][4 * j + 2] = fmaf(p, v.z, o[i][4 * j + 2]);
-              o[i][4 * j + 3] = fmaf(p, v.w, o[i][4 * j + 3]);
-            }
-          }
-      }
-      __syncwarp();
-    }
-    if (tid == 0) record_unit(A, g);
-    const size_t slot = seg_slot(A, g.unit, blockIdx.x);
-    float4* po = (g.b < 0 ? A.part_s : A.part_p) + slot * urows * (HD / 4);
-    float2* ml = (g.b < 0 ? A.ml_s : A.ml_p) + slot * urows;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i;
-      if (r >= nrows) continue;
-#pragma unroll
-      for (int j = 0; j < ND; ++j)
-        po[(size_t)(tx + 16 * j) * urows + r] =
-            make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
-      if (tx == 0) ml[r] = make_float2(m[i], l[i]);
-    }
+    if ((g.b < 0 ? A.srows : A.prows) <= kSimtFewRows)
+      simt_segment<HD, 1>(A, g, sm, s_pages);
+    else
+      simt_segment<HD, 4>(A, g, sm, s_pages);
   }
 }
 

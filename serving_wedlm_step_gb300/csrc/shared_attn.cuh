@@ -231,6 +231,7 @@ __device__ __forceinline__ const T* window_block(const SharedArgs& A, int b, int
 
 // fp32: urows query rows per unit, whatever tokens they belong to
 constexpr int kSimtRows = 64;
+constexpr int kSimtFewRows = 16;  // units of at most so many rows take smaller tiles
 cudaError_t launch_shared_attention_simt(const SharedArgs& A, int hd, cudaStream_t st);
 // bf16: units of 2 * TPB tokens, TPB = 128 / G
 cudaError_t launch_shared_attention_tc(const SharedArgs& A, int hd, int TPB, cudaStream_t st);
