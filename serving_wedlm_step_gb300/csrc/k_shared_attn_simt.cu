@@ -312,11 +312,14 @@ shared_attn_simt_kernel(const __grid_constant__ SharedArgs A) {
 // partials out among them and load four at a time with a running maximum, so that
 // few rows with many partials do not wait for them one by one (one token of 8
 // heads over 32768 shared positions, 150 partials a row: 23 us for the whole call
-// with a load at a time, 16 now).  Partials lie dims-major, so that both the
-// writer's warps (a lane per row) and these loads touch runs of rows.
+// with a load at a time, 16 now).  Where rows abound, two at a time leave registers
+// for a third block per SM (64 x 32 rows over 16384: 398 -> 395 us).  Partials lie
+// dims-major, so that both the writer's warps (a lane per row) and these loads touch
+// runs of rows.
 template <typename T, int HD, int RPB>
 __global__ void __launch_bounds__(2 * HD) shared_merge_kernel(const __grid_constant__ SharedArgs A) {
-  constexpr int NG = 32 / RPB;       // lane groups of a row
+  constexpr int NG = 32 / RPB;           // lane groups of a row
+  constexpr int PF = RPB == 8 ? 4 : 2;   // partials loaded together
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, d40 = threadIdx.x / 32 * 4;
@@ -339,12 +342,12 @@ __global__ void __launch_bounds__(2 * HD) shared_merge_kernel(const __grid_const
   const float2* ml_p = A.ml_p + (size_t)seg_slot(A, up, bp.x) * A.prows + ip;
   const float4* o_s = A.part_s + ((size_t)seg_slot(A, us, bs.x) * (HD / 4) + d40) * A.srows + is;
   const float4* o_p = A.part_p + ((size_t)seg_slot(A, up, bp.x) * (HD / 4) + d40) * A.prows + ip;
-  // four of this lane's partials from i on, loaded together (none: a sum of 0)
-  float2 ml[4];
-  float4 v[4][4];
+  // PF of this lane's partials from i0 on (none: a sum of 0)
+  float2 ml[PF];
+  float4 v[PF][4];
   auto fetch = [&](int i0) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < PF; ++c) {
       const int i = i0 + c * NG;
       ml[c] = make_float2(-INFINITY, 0.f);
       if (i >= n) continue;
@@ -368,11 +371,14 @@ __global__ void __launch_bounds__(2 * HD) shared_merge_kernel(const __grid_const
     M = to;
   };
 #pragma unroll 1
-  for (int i = grp; i < n; i += 4 * NG) {
+  for (int i = grp; i < n; i += PF * NG) {
     fetch(i);
-    raise(fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x))));
+    float to = M;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < PF; ++c) to = fmaxf(to, ml[c].x);
+    raise(to);
+#pragma unroll
+    for (int c = 0; c < PF; ++c) {
       if (ml[c].y == 0.f) continue;  // no key seen (keys that are all NaN leave l NaN)
       const float w = exp2f(ml[c].x - M);
       l = fmaf(ml[c].y, w, l);

@@ -28,7 +28,7 @@
 //
 // What bounds it: a tile's softmax takes 1,340 cycles, and the other stream's
 // P V and S from hand-over to hand-over as long (1,024 of them MMAs).  64 x 32
-// rows of 32 heads over 16384 shared positions: 398 us, 1468 TFLOP/s.
+// rows of 32 heads over 16384 shared positions: 395 us, 1478 TFLOP/s.
 //
 // Single-thread instructions sit under elect.sync: under a comparison of the lane
 // number an MMA took 90-110 cycles to issue, under elect.sync it runs at the
