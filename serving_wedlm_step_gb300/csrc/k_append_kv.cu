@@ -189,10 +189,12 @@ append_kv_kernel(const __grid_constant__ AppendArgs A) {
           c[j] = c[j] * r * g2.get(j);
         }
       }
+      if (row) {  // a pad row stays zeros: neither eps = 0 nor the gain makes it NaN
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x1.set(j, a[j] * cs[j] - c[j] * sn[j]);
-        x2.set(j, c[j] * cs[j] + a[j] * sn[j]);
+        for (int j = 0; j < 8; ++j) {
+          x1.set(j, a[j] * cs[j] - c[j] * sn[j]);
+          x2.set(j, c[j] * cs[j] + a[j] * sn[j]);
+        }
       }
     }
     if (kind == 0) {
