@@ -128,10 +128,11 @@ append_kv_kernel(const __grid_constant__ AppendArgs A) {
   const int h1 = min(A.heads, h0 + A.heads_per_block);
   float cs[8], sn[8];
   if (h0 < A.heads - A.nkv) {  // some head of the run rotates
-    const int t = !row ? 0 : A.pos ? A.pos[(size_t)b * A.n + p] : (int)s;
+    // 64 bits: a length of nearly 2^31 plus p passes 32
+    const long long t = !row ? 0 : A.pos ? A.pos[(size_t)b * A.n + p] : s;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint64_t turn = (uint64_t)(int64_t)t * s_step[dg * 8 + j];
+      const uint64_t turn = (uint64_t)t * s_step[dg * 8 + j];
       // the top 32 bits as a signed fraction of a turn: 2 * it half turns
       sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn[j], &cs[j]);
     }

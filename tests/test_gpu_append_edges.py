@@ -1,12 +1,12 @@
-"""wedlm_append_kv at the edges: rms_eps, pad rows of the window block, lengths on
-either side of a page's end."""
+"""wedlm_append_kv at the edges: rms_eps, pad rows of the window block, positions
+past 32 bits, lengths on either side of a page's end."""
 import functools
 
 import pytest
 import torch
 
 from tests import test_gpu_append_kv as base
-from tests.paged_common import PAGE, block_rows, rotate
+from tests.paged_common import PAGE, block_rows, rotate, rotate_bound
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float32
@@ -45,6 +45,28 @@ def test_eps_enters_the_norm(monkeypatch, dtype, hd, eps, scale):
     before = c.pool.clone()
     c.call(rms_eps=eps)
     c.check(before)
+
+
+def test_positions_past_32_bits():
+    """Without `pos` a row's position is seq_len + p, also where that passes 2^31 - 1:
+    nothing can be appended there, but the queries are rotated."""
+    from serving_wedlm_step_gb300 import binding as Bd
+    c = base.Case(2, 3, 4, 2, 128, FP, 0, None, True, False, False, seed=23)
+    far = [(1 << 31) - 1, (1 << 31) - 2]
+    c.seq_len.copy_(torch.tensor(far, dtype=torch.int32))
+    before = c.pool.clone()
+    c.call()
+    torch.cuda.synchronize()
+    assert int(c.err) == Bd.DEV_CAPACITY and c.new_len.tolist() == far
+    assert torch.equal(c.pool, before)
+    for b in range(2):
+        t = torch.arange(3, device="cuda") + far[b]
+        y, mag = rotate(c.q[b], t, c.theta)
+        got = c.q_out[b * 3:(b + 1) * 3].double()
+        assert ((got - y).abs() <= rotate_bound(y, mag, FP)).all()
+        y, mag = rotate(c.k[b], t, c.theta)
+        got = block_rows(c.win[b], 128)[0, :, :3].transpose(0, 1).double()
+        assert ((got - y).abs() <= rotate_bound(y, mag, FP)).all()
 
 
 def test_more_rows_than_a_page_stay_in_their_pages():
