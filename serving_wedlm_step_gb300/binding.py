@@ -475,9 +475,13 @@ def _take_rows(name, t, dev, dtype, B, n, heads, hd):
 
 
 def _pool_pages(pool, n_kv, hd):
-    pages, rest = divmod(pool.numel(), 32 * n_kv * hd)
-    if rest or not pages:
-        raise _bad_arg(f"the pool must hold whole pages of {32 * n_kv * hd} values")
+    """Pages of a pool [pages][2][n_kv][16*hd], trailing dims split or joined."""
+    page, shape = 32 * n_kv * hd, pool.shape
+    pages, rest = divmod(pool.numel(), page)
+    if rest or not pages or (len(shape) > 1 and shape[0] != pages) or \
+            (len(shape) > 2 and shape[1] != 2) or (len(shape) > 3 and shape[2] != n_kv):
+        raise _bad_arg(f"the pool must hold whole pages [2][{n_kv}][{16 * hd}], not "
+                       f"{tuple(shape)}")
     return pages
 
 
@@ -503,10 +507,10 @@ def append_kv(k, v, pool, page_table, seq_len, counts=None, pos=None, q=None, q_
 
     k, v: [B][n][n_kv][hd], q: [B][n][n_q][hd], bf16 or fp32, any strides whose
     rows are 16-byte aligned (slices of one packed projection, say).  pool: one
-    layer's pages; page_table int32 [B][max_pages]; seq_len, counts,
-    new_seq_len int32 [B]; pos int32 [B][n]; q_out [B*n][n_q][hd]; kv_win
-    [B][2][n_kv][Wp*hd]; k_norm, q_norm [hd]; error: int32 [1] that the
-    WEDLM_DEV_* bits are OR-ed into.  The tensors' device need not be the
+    layer's pages [pages][2][n_kv][16*hd]; page_table int32 [B][max_pages];
+    seq_len, counts, new_seq_len int32 [B]; pos int32 [B][n]; q_out
+    [B*n][n_q][hd]; kv_win [B][2][n_kv][Wp*hd]; k_norm, q_norm [hd]; error:
+    int32 [1] that the WEDLM_DEV_* bits are OR-ed into.  The tensors' device need not be the
     current one; the stream is that device's current stream, or `stream`."""
     import torch
     if not k.is_cuda or k.dim() != 4:
@@ -545,12 +549,13 @@ def shared_prefix_attention(q, pool, shared_pages, page_table, seq_len, kv_win, 
     """wedlm_shared_attention: window attention of a batch whose sequences share
     the positions of `shared_pages` (int32 [S], or None), computed once for all.
 
-    q: [B*W][n_q][hd] (RoPE applied); pool: one layer's pages; page_table int32
-    [B][max_pages]; seq_len int32 [B], shared part included; kv_win
-    [B][2][n_kv][Wp*hd]; o: [B*W][n_q*hd], returned.  workspace: a byte tensor
-    of at least shared_prefix_workspace() bytes that no overlapping call uses;
-    by default one is taken from torch's allocator, on the call's stream.  The
-    tensors' device need not be the current one."""
+    q: [B*W][n_q][hd] (RoPE applied); pool: one layer's pages
+    [pages][2][n_kv][16*hd]; page_table int32 [B][max_pages]; seq_len int32 [B],
+    shared part included; kv_win [B][2][n_kv][Wp*hd]; o: [B*W][n_q*hd],
+    returned.  workspace: a byte tensor of at least shared_prefix_workspace()
+    bytes that no overlapping call uses; by default one is taken from torch's
+    allocator, on the call's stream.  The tensors' device need not be the
+    current one."""
     import torch
     if not q.is_cuda or q.dim() != 3 or kv_win.dim() != 4 or seq_len.dim() != 1 or \
             page_table.dim() != 2:
