@@ -427,6 +427,11 @@ _SHARED_PACK = struct.Struct("@9i4x8PNP").pack
 _BYTES_FN = {}
 
 
+def _unpackable(e):
+    """The refusal of a value that is no number or a size past 2^31."""
+    return _bad_arg(f"an argument does not fit its field: {e}")
+
+
 def _bytes_fn(name):
     """The entry point `name`, its struct argument passed as bytes."""
     fn = _BYTES_FN.get(name)
@@ -529,16 +534,21 @@ def append_kv(k, v, pool, page_table, seq_len, counts=None, pos=None, q=None, q_
     if q is not None:
         nq = q.shape[2] if q.dim() == 4 else 0
         q_rows = _take_rows("q", q, dev, dt, B, n, nq, hd)
-    args = _APPEND_PACK(
-        B, n, nq, nkv, hd, code, cols, _pool_pages(pool, nkv, hd), rms_eps, rope_theta,
-        *_take_rows("k", k, dev, dt, B, n, nkv, hd), *_take_rows("v", v, dev, dt, B, n, nkv, hd),
-        *q_rows, _take("q_norm", q_norm, dev, dt, (hd,)), _take("k_norm", k_norm, dev, dt, (hd,)),
-        _take("pos", pos, dev, i32, (B, n)), _take("counts", counts, dev, i32, (B,)),
-        _take("seq_len", seq_len, dev, i32, (B,)),
-        _take("page_table", page_table, dev, i32, (B, cols)), _take("pool", pool, dev, dt),
-        _take("q_out", q_out, dev, dt, (B * n, nq, hd)),
-        _take("kv_win", kv_win, dev, dt, (B, 2, nkv, (n + 15) // 16 * 16 * hd)),
-        _take("new_seq_len", new_seq_len, dev, i32, (B,)), _take("error", error, dev, i32, (1,)))
+    try:
+        args = _APPEND_PACK(
+            B, n, nq, nkv, hd, code, cols, _pool_pages(pool, nkv, hd), rms_eps, rope_theta,
+            *_take_rows("k", k, dev, dt, B, n, nkv, hd),
+            *_take_rows("v", v, dev, dt, B, n, nkv, hd), *q_rows,
+            _take("q_norm", q_norm, dev, dt, (hd,)), _take("k_norm", k_norm, dev, dt, (hd,)),
+            _take("pos", pos, dev, i32, (B, n)), _take("counts", counts, dev, i32, (B,)),
+            _take("seq_len", seq_len, dev, i32, (B,)),
+            _take("page_table", page_table, dev, i32, (B, cols)), _take("pool", pool, dev, dt),
+            _take("q_out", q_out, dev, dt, (B * n, nq, hd)),
+            _take("kv_win", kv_win, dev, dt, (B, 2, nkv, (n + 15) // 16 * 16 * hd)),
+            _take("new_seq_len", new_seq_len, dev, i32, (B,)),
+            _take("error", error, dev, i32, (1,)))
+    except (struct.error, OverflowError) as e:
+        raise _unpackable(e) from None
     rc = _on_device(dev, _bytes_fn("wedlm_append_kv"), args, _raw_stream(dev, stream))
     if rc != OK:
         raise WedlmError(rc, "wedlm_append_kv failed")
@@ -575,20 +585,23 @@ def shared_prefix_attention(q, pool, shared_pages, page_table, seq_len, kv_win, 
             _take("kv_win", kv_win, dev, dt, (B, 2, nkv, (W + 15) // 16 * 16 * hd)),
             _take("o", o, dev, dt, (M, nq * hd)))
     err = _take("error", error, dev, i32, (1,))
-    if workspace is None:
-        need = _bytes_fn("wedlm_shared_attention_workspace")(
-            _SHARED_PACK(*sizes, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0))
-        if need == 0:
-            raise _bad_arg("sizes that wedlm_shared_attention does not take")
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        else:  # freed on return: its next user must come after this call on its stream
-            with torch.cuda.stream(stream):
+    try:
+        if workspace is None:
+            need = _bytes_fn("wedlm_shared_attention_workspace")(
+                _SHARED_PACK(*sizes, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0))
+            if need == 0:
+                raise _bad_arg("sizes that wedlm_shared_attention does not take")
+            if stream is None:
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise _bad_arg(f"workspace must be a contiguous tensor on cuda:{dev}")
-    args = _SHARED_PACK(*sizes, *ptrs, workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), err)
+            else:  # freed on return: its next user must come after this call on its stream
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise _bad_arg(f"workspace must be a contiguous tensor on cuda:{dev}")
+        args = _SHARED_PACK(*sizes, *ptrs, workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), err)
+    except (struct.error, OverflowError) as e:
+        raise _unpackable(e) from None
     rc = _on_device(dev, _bytes_fn("wedlm_shared_attention"), args, _raw_stream(dev, stream))
     if rc != OK:
         raise WedlmError(rc, "wedlm_shared_attention failed")

@@ -1,5 +1,5 @@
-"""The pool shapes that the binding of the append and of the shared-prefix
-attention takes and refuses."""
+"""What the binding of the append and the shared-prefix attention refuses for a
+pool's shape and for numbers that the C structs do not hold."""
 import pytest
 import torch
 
@@ -64,3 +64,31 @@ def test_attention_takes_a_pool_of_its_own_shape_only():
             c.call(o)
         torch.cuda.synchronize()
         assert e.value.code == Bd.ERR_INVALID_ARG and o.isnan().all(), shape
+
+
+@pytest.mark.parametrize("bad", [dict(rope_theta=1e39), dict(rms_eps=1e39), dict(rope_theta=-1e39),
+                                 dict(rope_theta="1e6"), dict(rms_eps=None)])
+def test_numbers_that_32_bits_do_not_hold_are_refused(bad):
+    from serving_wedlm_step_gb300 import binding as Bd
+    c = base.Case(1, 2, 4, 2, 64, FP, 0, None, True, True, False, seed=33)
+    before = c.pool.clone()
+    with pytest.raises(Bd.WedlmError) as e:
+        c.call(**bad)
+    torch.cuda.synchronize()
+    assert e.value.code == Bd.ERR_INVALID_ARG and torch.equal(c.pool, before)
+
+
+def test_sizes_that_32_bits_do_not_hold_are_refused():
+    """Rows expanded from one, and a page table of 2^31 columns."""
+    from serving_wedlm_step_gb300 import binding as Bd
+    c = base.Case(1, 1, 0, 2, 64, FP, 0, None, False, False, False, seed=34)
+    c.k, c.v = (t.expand(1, 1 << 31, 2, 64) for t in (c.k, c.v))
+    with pytest.raises(Bd.WedlmError) as e:
+        c.call()
+    assert e.value.code == Bd.ERR_INVALID_ARG
+    a = AttnCase([16 * 3 + 5], 4, 4, 2, 64, 3, BF, seed=35)
+    a.table = torch.empty(1, 1 << 31, dtype=torch.int32, device="cuda")  # 8 GB, not read
+    for kw in (dict(), dict(workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(Bd.WedlmError) as e:
+            a.call(**kw)
+        assert e.value.code == Bd.ERR_INVALID_ARG
