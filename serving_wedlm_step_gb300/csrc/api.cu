@@ -1128,7 +1128,10 @@ int wedlm_attention(wedlm_ctx* c, int32_t batch, const void* q, const void* kv_p
   cudaError_t e;
   {
     Timed t(c, WEDLM_KIND_ATTN, st);
-    e = g.dtype == WEDLM_BF16 ? run_attention<bf16>(c, A, st)
+    // Not launched early, as within a step: the kernel reads lengths, page ids and
+    // pages before it waits, and here the caller's kernel in front (an append, say)
+    // may have written them.
+    e = g.dtype == WEDLM_BF16 ? launch_attention_tc(A, c->zero_page, c->num_sms, st, false)
                               : run_attention<float>(c, A, st);
   }
   if (e != cudaSuccess) return fail(c, WEDLM_ERR_CUDA, cudaGetErrorString(e));

@@ -73,8 +73,10 @@ __device__ __forceinline__ int tile_off(int t, int d, int hd) {
 // reading anything that kernel wrote, and before writing anything, it calls
 // pdl_wait (which returns once the previous kernel has completed and its
 // memory is visible), then pdl_trigger lets the next kernel start early in
-// turn.  Work on data no kernel of the step writes (weights, cached KV pages,
-// page tables) may go before pdl_wait.
+// turn.  Work on data that the kernel in front does not write may go before
+// pdl_wait: weights, and within a step page tables and the cached pages below
+// seq_len.  Kernels that a caller's own calls may precede (wedlm_attention,
+// which reads pages that wedlm_append_kv or the caller wrote) are launched without it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -75,9 +75,8 @@ append_kv_kernel(const __grid_constant__ AppendArgs A) {
   constexpr int RB = kAppendThreads / DG;
   __shared__ uint64_t s_step[HD / 2];
   if (threadIdx.x < HD / 2) s_step[threadIdx.x] = A.step[threadIdx.x];
-  // The rows and lengths come from earlier kernels.  No pdl_trigger: the
-  // window attention reads cached pages before it waits for the kernel in
-  // front of it, so it must not start before these pages are written.
+  // The rows and lengths come from earlier kernels.  No pdl_trigger: nothing
+  // starts before the pages and lengths written here are there.
   pdl_wait();
   __syncthreads();
 
