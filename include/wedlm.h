@@ -436,7 +436,7 @@ typedef struct wedlm_shared_attn_args {
   int32_t n_q_heads, n_kv_heads; /* n_kv_heads 1..1024, their ratio G 1..128 */
   int32_t head_dim;            /* 64 or 128                                */
   int32_t dtype;               /* WEDLM_BF16 | WEDLM_FP32                  */
-  int32_t n_shared_pages;      /* S >= 0 pages of shared prefix            */
+  int32_t n_shared_pages;      /* S, 0..2^26 pages of shared prefix        */
   int32_t max_pages_per_seq;   /* columns of page_table, 1..2^26           */
   int32_t num_pages;           /* pages in kv_pool                         */
   const void *q;               /* [B*W][n_q_heads][head_dim], RoPE applied */
@@ -478,9 +478,13 @@ size_t wedlm_shared_attention_workspace(const wedlm_shared_attn_args *args);
  *    bit for bit, whenever the inputs are.
  *  - q, kv_pool, kv_win and o are 16-byte aligned and contiguous; o and the
  *    workspace overlap no input and not each other.
- *  - Limit: n_kv_heads * (row blocks of the batch * S/8 + B * row blocks of a
- *    window * max_pages_per_seq/8) stays below 2^31 (a row block: 128 rows or
- *    more in bf16, 64 in fp32, of the G rows per token).
+ *  - Scores, maxima, sums and O are held in fp32.  In bf16 a probability is
+ *    rounded to bf16 before it meets V, as in wedlm_attention (half a step of
+ *    it, 2^-8, beside the output's own rounding).
+ *  - Limits, with u rows a unit (bf16: 2 * floor(128/G) * G, fp32: 64),
+ *    R = ceil(B*W*G / u) and r = ceil(W*G / u): n_kv_heads * (R + B*r) <= 2^24
+ *    and n_kv_heads * (R * (1 + ceil(S/8)) + B*r * (1 + ceil((max_pages_per_seq
+ *    + ceil(W/16)) / 8))) < 2^31.  Beyond either a call is refused.
  * Returns WEDLM_ERR_INVALID_ARG (nothing enqueued), WEDLM_ERR_CAPACITY for a
  * workspace that is too small, or WEDLM_ERR_CUDA. */
 int wedlm_shared_attention(const wedlm_shared_attn_args *args, void *stream);
