@@ -189,12 +189,14 @@ append_kv_kernel(const __grid_constant__ AppendArgs A) {
           c[j] = c[j] * r * g2.get(j);
         }
       }
-      if (row) {  // a pad row stays zeros: neither eps = 0 nor the gain makes it NaN
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x1.set(j, a[j] * cs[j] - c[j] * sn[j]);
-          x2.set(j, c[j] * cs[j] + a[j] * sn[j]);
-        }
+      for (int j = 0; j < 8; ++j) {
+        x1.set(j, a[j] * cs[j] - c[j] * sn[j]);
+        x2.set(j, c[j] * cs[j] + a[j] * sn[j]);
+      }
+      if (!row) {  // neither eps = 0 nor the gain makes a pad row NaN
+        x1.zero();
+        x2.zero();
       }
     }
     if (kind == 0) {
