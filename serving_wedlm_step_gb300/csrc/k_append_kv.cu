@@ -299,8 +299,11 @@ extern "C" int wedlm_append_kv(const wedlm_append_args* a, void* stream) {
   // A block walks over a run of heads with one set of angles.  Long runs spare
   // angles; but while the row blocks alone leave the GPU idle the runs are cut, for
   // a block's time is its run's latency: one token of 32 + 8 + 8 heads took 23 us
-  // in one run.  8 blocks of 128 threads are resident per SM.
-  const int64_t want = 8 * 152;
+  // in one run.  8 blocks an SM are about what is resident (7 in bf16 with 72
+  // registers, 5 in fp32 with 91).
+  const int sms = device_sms();
+  if (sms < 1) return WEDLM_ERR_CUDA;
+  const int64_t want = 8 * (int64_t)sms;
   A.heads_per_block = (int)std::max<int64_t>(1, std::min<int64_t>(A.heads, A.heads * gx / want));
   const int gy = (A.heads + A.heads_per_block - 1) / A.heads_per_block;
   if (gy > 65535) return WEDLM_ERR_INVALID_ARG;

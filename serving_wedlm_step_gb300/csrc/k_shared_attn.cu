@@ -2,7 +2,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "shared_attn.cuh"
 
@@ -10,17 +9,6 @@ namespace wedlm {
 namespace {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-
-// SMs of the current device (asked once per device), 0 when there is none
-int device_sms() {
-  static std::atomic<int> known[64];
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
-  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
-  return sms;
-}
 
 // Sizes of a call: its split and the workspace's layout.  False for sizes the
 // kernels do not take.
