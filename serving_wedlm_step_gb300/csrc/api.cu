@@ -1125,13 +1125,11 @@ int wedlm_attention(wedlm_ctx* c, int32_t batch, const void* q, const void* kv_p
   c->last_stream = st;
   AttnArgs A = attn_args(c, batch, ctx_win(c), q, kv_pool, page_table, seq_len, num_pages,
                          kv_win, o);
+  A.wait_first = 1;  // a caller's kernel (an append, say) may stand in front
   cudaError_t e;
   {
     Timed t(c, WEDLM_KIND_ATTN, st);
-    // Not launched early, as within a step: the kernel reads lengths, page ids and
-    // pages before it waits, and here the caller's kernel in front (an append, say)
-    // may have written them.
-    e = g.dtype == WEDLM_BF16 ? launch_attention_tc(A, c->zero_page, c->num_sms, st, false)
+    e = g.dtype == WEDLM_BF16 ? run_attention<bf16>(c, A, st)
                               : run_attention<float>(c, A, st);
   }
   if (e != cudaSuccess) return fail(c, WEDLM_ERR_CUDA, cudaGetErrorString(e));

@@ -75,8 +75,8 @@ __device__ __forceinline__ int tile_off(int t, int d, int hd) {
 // memory is visible), then pdl_trigger lets the next kernel start early in
 // turn.  Work on data that the kernel in front does not write may go before
 // pdl_wait: weights, and within a step page tables and the cached pages below
-// seq_len.  Kernels that a caller's own calls may precede (wedlm_attention,
-// which reads pages that wedlm_append_kv or the caller wrote) are launched without it.
+// seq_len.  Where a caller's own calls may stand in front (wedlm_attention reads
+// pages that wedlm_append_kv or the caller wrote) it may not.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -158,6 +158,9 @@ struct AttnArgs {
   int pt_stride;        // page-table row of sequence b starts at b * pt_stride
                         // (max_pages; 0: every sequence reads row 0)
   int kv_reuse;         // 1: pages are read by many units (keep them in L2)
+  int wait_first;       // 1: the kernel in front may have written lengths, page ids or
+                        // pages: wait for it before they are read (else only q and the
+                        // window block, as within a step)
   float scale_log2;     // log2(e) / sqrt(hd)
   const void* q;        // [B*W][nq][hd]
   const void* pool;     // this layer's pool

@@ -233,6 +233,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, AttnArgs A, AttnLayout Ly
   // (the tiles of unit u inside block c) has slot u + c: along the tile
   // order neither u nor c ever decreases and one of them grows from one
   // segment to the next, so slots are distinct and fewer than units + G.
+  if (A.wait_first) pdl_wait();
   for (int b = threadIdx.x; b < A.B; b += kThreads) s_P[b] = prefix_tiles(A, b);
   __syncthreads();
   const int ucost = max(0, A.unit_cost);
