@@ -46,18 +46,19 @@ bool shared_plan(const wedlm_shared_attn_args& a, SharedPlan* P) {
   if (a.dtype == WEDLM_BF16) {
     // relative times, swept on GB300: a tile for 128 rows 16, for a pair of row
     // blocks 28; a unit's start and end 32, more with the rows whose partial it
-    // writes.  (When this was first swept, all tiles alike and ends 12 took 579 us
-    // for 64 sequences x 32 rows over 16384 shared positions, these 416; 64 single
-    // tokens over 8192 with pairs at 20 took 47 us, with these 40.  Later 400 and
-    // 39, pairs at 24 to 32 or ends at 24 to 48 within 2 % and 14 % of them.)
+    // writes.  64 x 32 rows over 16384 shared positions: 399 us with these, 397 to 404
+    // with ends at 16 to 64, 411 with pairs at 20; heads of 64: 362, 359 to 367, 375.
+    // 64 single tokens over 8192: 36.9 us, 41 to 43, 45.5; heads of 64: 33.6, 35 to
+    // 39, 40.5.  Pairs at 32 are within 5 % on all of these.
     A.ucost = 32 + std::min(A.prows, 128) / 4;
     A.shared_cost = A.B * A.W > P->TPB ? 28 : 16;
     A.private_cost = A.W > P->TPB ? 28 : 16;
     A.min_share = 32;
   } else {
-    // a tile of 64 rows 4, of 16 rows 2, a unit's ends 2 (swept with a slower merge:
-    // 12 sequences x 8 rows over 2048 shared positions 23.4 us, 24.5 with 16 rows at
-    // 3, 28.5 with all at 1)
+    // a tile of 64 rows 4, of 16 rows 2, a unit's ends 2, swept on GB300.  12 sequences
+    // x 8 rows over 2048 shared positions, heads of 64: 20.8 us with these, 26.3 with
+    // ends at 1, 20.9 at 4, 26.5 at 6; a 64-row tile at 3 20.9, at 6 26.1, at 8 28.8.
+    // 16 x 32 rows over 8192: 289 us, 298, 283, 283; 284, 291, 303; heads of 128 within 3 %
     A.ucost = 2;
     A.shared_cost = A.srows > kSimtFewRows ? 4 : 2;
     A.private_cost = A.prows > kSimtFewRows ? 4 : 2;

@@ -9,9 +9,11 @@
 // and 4 rows x 8 (4) dims of O, so a step of 4 dims (keys) does 128 FMAs, in
 // pairs, on 12 shared-memory vectors.  K, V and Q rows are padded by 4 floats: 8
 // lanes that read 8 rows touch 32 different banks.  V comes during S, the next K
-// during P V.  What bounds it is the latency of the shared-memory reads, with two
-// warps a scheduler: 40 sequences x 32 rows of 4 heads of 128 over 8192 shared
-// positions 590 us, 37 TFLOP/s (FMAs one by one 618 us).
+// during P V.  What bounds it is latency, with two warps a scheduler (an issue slot
+// in three is used; the warps wait for shared memory and for the results of their own
+// arithmetic): 40 sequences x 32 rows of 4 heads of 128 over 8192 shared positions and
+// up to 700 of their own 604 us, 37 TFLOP/s of the 80 that FMAs alone could do; 16 x 32
+// rows of 8 heads of 64, 2 kv heads, 289 us, 31 TFLOP/s.
 //
 // Units of at most 16 rows (a window's own keys, most often) take tiles of 16 rows,
 // one a thread: 12 sequences x 8 rows of 4 heads of 64 over 2048 shared positions
@@ -312,8 +314,8 @@ shared_attn_simt_kernel(const __grid_constant__ SharedArgs A) {
 // partials out among them and load four at a time with a running maximum, so that
 // few rows with many partials do not wait for them one by one (one token of 8
 // heads over 32768 shared positions, 150 partials a row: 23 us for the whole call
-// with a load at a time, 16 now).  Where rows abound, two at a time leave registers
-// for a third block per SM (64 x 32 rows over 16384: 398 -> 395 us).  Partials lie
+// with a load at a time, 16 so).  Where rows abound, two at a time leave registers
+// for a third block per SM (3 us of 64 x 32 rows over 16384).  Partials lie
 // dims-major, so that both the writer's warps (a lane per row) and these loads touch
 // runs of rows.
 template <typename T, int HD, int RPB>
@@ -429,9 +431,13 @@ cudaError_t launch_simt(const SharedArgs& A, cudaStream_t st) {
 template <typename T, int HD>
 cudaError_t launch_merge(const SharedArgs& A, cudaStream_t st) {
   const int rows = A.B * A.W * A.G;
-  // 8 rows a block while that leaves the GPU room, 32 (whole 512-byte runs) beyond:
-  // 4096 rows of all kv heads 24.2 us a call with 8, 27.5 with 32; 8192 rows 110.3
-  // and 108.0
+  // 8 rows a block while that leaves the GPU room, 32 (whole 512-byte runs) beyond.
+  // Whole calls with 8 and with 32, by rows of all kv heads, us:
+  //                                   2048       4096       6144       8192      16384
+  //   heads of 128, 256 shared    13.8 15.7  16.0 15.6  17.8 16.0  19.6 16.3  32.6 23.5
+  //   heads of 128, 8192 shared   22.0 31.1  29.4 32.8  36.9 36.7  45.5 43.3  76.2 68.0
+  //   heads of 64, 256 shared     12.3 13.3  12.5 13.6  14.1 13.6  14.4 13.6  22.5 18.7
+  //   heads of 64, 8192 shared    18.5 24.2  23.6 26.9  30.7 31.5  37.2 37.3  63.7 60.9
   if ((long long)rows * A.nkv <= 6 * 1024)
     return launch_pdl(shared_merge_kernel<T, HD, 8>, dim3((rows + 7) / 8, A.nkv), dim3(2 * HD), 0,
                       st, A);

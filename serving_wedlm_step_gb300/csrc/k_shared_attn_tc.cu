@@ -26,9 +26,12 @@
 // and its queue is short, so what one issuer spends on waits and descriptors is
 // time the other's MMAs run.
 //
-// What bounds it: a tile's softmax takes 1,340 cycles, and the other stream's
-// P V and S from hand-over to hand-over as long (1,024 of them MMAs).  64 x 32
-// rows of 32 heads over 16384 shared positions: 395 us, 1478 TFLOP/s.
+// What bounds it: the softmax.  A tile's takes its eight warps 1,340 cycles, and the
+// warps take the streams' tiles in turn, so a round of two tiles is 2,680; the MMAs
+// of a round are 2,048 with heads of 128 and 1,024 with heads of 64.  64 x 32 rows of
+// 32 heads over 16384 shared positions: heads of 128 401 us, 1457 TFLOP/s (425 us
+// in a run of half a second, where the power limit takes the SMs from 2070 to some
+// 1880 MHz), heads of 64 361 us, 809 TFLOP/s.
 //
 // Single-thread instructions sit under elect.sync: under a comparison of the lane
 // number an MMA took 90-110 cycles to issue, under elect.sync it runs at the
