@@ -563,9 +563,9 @@ def shared_prefix_attention(q, pool, shared_pages, page_table, seq_len, kv_win, 
     [pages][2][n_kv][16*hd]; page_table int32 [B][max_pages]; seq_len int32 [B],
     shared part included; kv_win [B][2][n_kv][Wp*hd]; o: [B*W][n_q*hd],
     returned.  workspace: a byte tensor of at least shared_prefix_workspace()
-    bytes that no overlapping call uses; by default one is taken from torch's
-    allocator, on the call's stream.  The tensors' device need not be the
-    current one."""
+    bytes, 256-byte aligned, that no overlapping call uses; by default one is
+    taken from torch's allocator, on the call's stream.  The tensors' device
+    need not be the current one."""
     import torch
     if not q.is_cuda or q.dim() != 3 or kv_win.dim() != 4 or seq_len.dim() != 1 or \
             page_table.dim() != 2:
