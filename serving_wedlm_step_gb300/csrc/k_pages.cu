@@ -279,18 +279,23 @@ constexpr int kPlan = 1024, kPlanWarps = kPlan / 32;
 constexpr int kFewPages = 2048;     // that a plan lists in shared memory
 constexpr int kScan = 8;            // counts of a thread in flight
 constexpr int kManyPages = 1 << 14, kPlanBlocks = 8;
+// Sums stop at kSumCap.  Needs of 1024 rows of up to 2^26 columns add up to 2^36, but what
+// is beyond the number of pages is all the same; min(a + b, cap) is associative, so that a
+// sum below the cap is exact and one beyond it is the cap, in any order.
+constexpr int kSumCap = kMaxPages + 1;
 
+// inclusive sum over the warp, values 0..kSumCap
 __device__ __forceinline__ int warp_incl(int v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+    if (lane >= o) v = min(v + u, kSumCap);
   }
   return v;
 }
 
-// inclusive sum over the block's threads; `sums` [kPlanWarps + 1], the total in the last
+// the same over the block's threads; `sums` [kPlanWarps + 1], the total in the last
 __device__ int block_incl(int v, int* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   v = warp_incl(v);
@@ -304,7 +309,7 @@ __device__ int block_incl(int v, int* sums) {
     if (lane == 31) sums[kPlanWarps] = s;
   }
   __syncthreads();
-  return v + (warp ? sums[warp - 1] : 0);
+  return min(v + (warp ? sums[warp - 1] : 0), kSumCap);
 }
 
 // all threads of the cluster; what they wrote is seen by all of it
@@ -680,7 +685,7 @@ int64_t copy_items(const wedlm_page_pools& p, int64_t pages) {
 bool page_state_ok(const wedlm_page_state& s, int max_batch, bool uses_len, bool new_len,
                    std::initializer_list<PageSpan> inputs, std::initializer_list<PageSpan> outputs) {
   if (s.batch < 1 || s.batch > max_batch || s.max_pages_per_seq < 1 ||
-      s.max_pages_per_seq > (1 << 26) || s.num_pages < 1 || s.num_pages > (1 << 28) ||
+      s.max_pages_per_seq > kMaxColumns || s.num_pages < 1 || s.num_pages > kMaxPages ||
       bad4(s.page_table) || bad4(s.page_refs) || bad4(s.new_page_table) ||
       bad4(s.new_page_refs) || (uses_len && bad4(s.seq_len)) || (new_len && bad4(s.new_seq_len)) ||
       odd4(s.error))
@@ -902,14 +907,14 @@ PageSpace compact_space(const wedlm_compact_args& a) {
 bool reserve_sizes(const wedlm_reserve_args& a) {
   const wedlm_page_state& s = a.state;
   return s.batch >= 1 && s.batch <= kReserveMaxBatch && s.max_pages_per_seq >= 1 &&
-         s.max_pages_per_seq <= (1 << 26) && s.num_pages >= 1 && s.num_pages <= (1 << 28) &&
+         s.max_pages_per_seq <= kMaxColumns && s.num_pages >= 1 && s.num_pages <= kMaxPages &&
          a.rows >= 0 && page_pools_ok(a.pools, true);
 }
 
 bool compact_sizes(const wedlm_compact_args& a) {
   const wedlm_page_state& s = a.state;
   return s.batch >= 1 && s.batch <= kPageMaxBatch && s.max_pages_per_seq >= 1 &&
-         s.max_pages_per_seq <= (1 << 26) && s.num_pages >= 1 && s.num_pages <= (1 << 28) &&
+         s.max_pages_per_seq <= kMaxColumns && s.num_pages >= 1 && s.num_pages <= kMaxPages &&
          a.max_moves >= -1 && page_pools_ok(a.pools, true);
 }
 }  // namespace

@@ -9,6 +9,8 @@ namespace wedlm {
 
 constexpr int kPageMaxBatch = 4096;
 constexpr int kReserveMaxBatch = 1024;
+constexpr int kMaxColumns = 1 << 26;  // of a page table
+constexpr int kMaxPages = 1 << 28;
 
 // wedlm_page_state with the error word; the kernels read the old arrays and write
 // the new ones, which may be the same
