@@ -718,7 +718,7 @@ def _page_pools(pools, dev, N):
         if pools.get_device() != dev or len(shape) < 3 or not pools.is_contiguous():
             raise _bad_arg(f"pools must be a contiguous tensor [layers][pages][..] on cuda:{dev}")
         n, pages = shape[0], shape[1]
-        step = pools.stride(0) * pools.element_size()
+        step = pools.numel() // max(n, 1) * pools.element_size()  # stride(0) of one layer is anything
         fields, keep = (0, pools.data_ptr(), step), None
     else:
         one = pools[0] if len(pools) else None
