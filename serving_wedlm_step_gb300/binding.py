@@ -728,8 +728,8 @@ def _page_pools(pools, dev, N):
         step = one.numel() * one.element_size()
         keep = (c_void_p * n)(*[_take("a pool", p, dev, one.dtype, one.shape) for p in pools])
         fields = ctypes.addressof(keep), 0, 0
-    if pages != N or step < N:
-        raise _bad_arg(f"the pools must have the {N} pages that page_refs counts")
+    if N == 0 or pages != N or step < N:
+        raise _bad_arg(f"the pools must have the pages that page_refs counts ({N}), at least one")
     return (n, step // N, *fields), keep
 
 

@@ -29,3 +29,13 @@ def test_page_bytes_follow_the_shape(Bd, layers, pages):
         assert (n, page_bytes, base, step) == (layers, page, p.data_ptr(), pages * page)
     (n, page_bytes, _, _, _), _ = Bd._page_pools(list(pool), HOST, pages)
     assert (n, page_bytes) == (layers, page)
+
+
+@pytest.mark.parametrize("pools", [torch.zeros(2, 0, 64), torch.zeros(0, 0, 64), torch.zeros(0, 4, 64),
+                                   torch.zeros(2, 4, 0), [torch.zeros(0, 64)], [torch.zeros(4, 0)], [],
+                                   [torch.zeros(4, 64), torch.zeros(0, 64)]])
+@pytest.mark.parametrize("N", [0, 4])
+def test_empty_pools_are_refused(Bd, pools, N):
+    with pytest.raises(Bd.WedlmError) as e:
+        Bd._page_pools(pools, HOST, N)
+    assert e.value.code == Bd.ERR_INVALID_ARG
