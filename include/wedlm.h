@@ -513,7 +513,8 @@ typedef struct wedlm_page_state {
                                   into, or NULL; never cleared here        */
 } wedlm_page_state;
 
-/* The pools whose pages the page table names, one per layer. */
+/* The pools whose pages the page table names, one per layer.  The calls that take
+ * them write them: no other array of the call lies in one. */
 typedef struct wedlm_page_pools {
   int32_t n_layers;            /* 1..64                                    */
   int64_t page_bytes;          /* 2*n_kv_heads*16*head_dim values of the

@@ -732,6 +732,33 @@ bool page_pools_ok(const wedlm_page_pools& p, bool sizes_only) {
   return true;
 }
 
+bool page_pools_apart(const wedlm_page_pools& p, const wedlm_page_state& s, bool uses_len,
+                      std::initializer_list<PageSpan> others) {
+  const uintptr_t bytes = (uintptr_t)s.num_pages * (uintptr_t)p.page_bytes;
+  auto pool = [&](int l) {
+    return p.kv_pools ? reinterpret_cast<uintptr_t>(p.kv_pools[l])
+                      : reinterpret_cast<uintptr_t>(p.base) + l * (uintptr_t)p.layer_stride;
+  };
+  uintptr_t low = pool(0), high = low;
+  for (int l = 1; l < p.n_layers; ++l) {
+    low = std::min(low, pool(l));
+    high = std::max(high, pool(l));
+  }
+  auto apart = [&](const void* x, int64_t ints) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = a + 4 * (uintptr_t)ints;
+    if (!a || b <= low || a >= high + bytes) return true;  // outside of all of them: most are
+    for (int l = 0; l < p.n_layers; ++l)
+      if (a < pool(l) + bytes && pool(l) < b) return false;
+    return true;
+  };
+  const int64_t cells = (int64_t)s.batch * s.max_pages_per_seq;
+  bool ok = apart(s.page_table, cells) && apart(s.new_page_table, cells) &&
+            apart(s.page_refs, s.num_pages) && apart(s.new_page_refs, s.num_pages) &&
+            apart(s.error, 1) && (!uses_len || apart(s.seq_len, s.batch));
+  for (const PageSpan& x : others) ok = ok && apart(x.p, x.n);
+  return ok;
+}
+
 PageArrays page_arrays(const wedlm_page_state& s) {
   PageArrays S;
   S.B = s.batch;
@@ -931,7 +958,12 @@ extern "C" int wedlm_reserve_pages(const wedlm_reserve_args* a, void* stream) {
   if (!page_state_ok(a->state, kReserveMaxBatch, true, false, {{a->counts, a->state.batch}},
                      {{a->granted, a->state.batch},
                       {a->n_free, 1},
-                      {a->workspace, (int64_t)(w.bytes / 4)}}))
+                      {a->workspace, (int64_t)(w.bytes / 4)}}) ||
+      !page_pools_apart(a->pools, a->state, true,
+                        {{a->counts, a->state.batch},
+                         {a->granted, a->state.batch},
+                         {a->n_free, 1},
+                         {a->workspace, (int64_t)(w.bytes / 4)}}))
     return WEDLM_ERR_INVALID_ARG;
   if (a->workspace_bytes < w.bytes) return WEDLM_ERR_CAPACITY;
   const int sms = device_sms();
@@ -971,7 +1003,11 @@ extern "C" int wedlm_compact_pages(const wedlm_compact_args* a, void* stream) {
   if (!page_state_ok(a->state, kPageMaxBatch, false, false, {},
                      {{a->page_map, a->state.num_pages},
                       {a->n_live, 1},
-                      {a->workspace, (int64_t)(w.bytes / 4)}}))
+                      {a->workspace, (int64_t)(w.bytes / 4)}}) ||
+      !page_pools_apart(a->pools, a->state, false,
+                        {{a->page_map, a->state.num_pages},
+                         {a->n_live, 1},
+                         {a->workspace, (int64_t)(w.bytes / 4)}}))
     return WEDLM_ERR_INVALID_ARG;
   if (a->workspace_bytes < w.bytes) return WEDLM_ERR_CAPACITY;
   const int sms = device_sms();
