@@ -514,7 +514,8 @@ typedef struct wedlm_page_state {
 } wedlm_page_state;
 
 /* The pools whose pages the page table names, one per layer.  The calls that take
- * them write them: no other array of the call lies in one. */
+ * them write them: no other array of the call lies in one, and two of them are apart or,
+ * for layers that share a cache, the same. */
 typedef struct wedlm_page_pools {
   int32_t n_layers;            /* 1..64                                    */
   int64_t page_bytes;          /* 2*n_kv_heads*16*head_dim values of the

@@ -741,8 +741,12 @@ bool page_pools_apart(const wedlm_page_pools& p, const wedlm_page_state& s, bool
   };
   uintptr_t low = pool(0), high = low;
   for (int l = 1; l < p.n_layers; ++l) {
-    low = std::min(low, pool(l));
-    high = std::max(high, pool(l));
+    const uintptr_t a = pool(l);
+    // one that layers share, or none of another's; below or above all others mostly
+    for (int k = a < high + bytes && low < a + bytes ? 0 : l; k < l; ++k)
+      if (a != pool(k) && a < pool(k) + bytes && pool(k) < a + bytes) return false;
+    low = std::min(low, a);
+    high = std::max(high, a);
   }
   auto apart = [&](const void* x, int64_t ints) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = a + 4 * (uintptr_t)ints;

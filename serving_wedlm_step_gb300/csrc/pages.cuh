@@ -38,7 +38,8 @@ struct PageSpan {
 bool page_state_ok(const wedlm_page_state& s, int max_batch, bool uses_len, bool new_len,
                    std::initializer_list<PageSpan> inputs, std::initializer_list<PageSpan> outputs);
 bool page_pools_ok(const wedlm_page_pools& p, bool sizes_only);
-// No array of the state and none of `others` lies in a pool: pools are read and written.
+// No array of the state and none of `others` lies in a pool (pools are read and written), and
+// no pool over a part of another.
 bool page_pools_apart(const wedlm_page_pools& p, const wedlm_page_state& s, bool uses_len,
                       std::initializer_list<PageSpan> others);
 PageArrays page_arrays(const wedlm_page_state& s);

@@ -36,3 +36,18 @@ def test_a_shared_pool_is_taken(Bd):  # noqa: F811
     same = (ctypes.c_void_p * 2)(64 * A, 64 * A)
     for pools in (dict(kv_pools=same), dict(kv_pools=None, base=64 * A, layer_stride=0)):
         assert call(Bd, "compact", make(Bd, "compact", workspace_bytes=0, **pools)) == Bd.ERR_CAPACITY
+
+
+@pytest.mark.parametrize("op", ARRAYS)
+def test_pools_over_one_another_are_refused(Bd, op):  # noqa: F811
+    """A page of one layer that is part of others of another layer: copies would race."""
+    for off in (16, 4096, POOL - 16):
+        for parts in ((64 * A, 64 * A + off), (64 * A + off, 64 * A)):
+            for pools in (dict(kv_pools=(ctypes.c_void_p * 2)(*parts)),
+                          dict(n_layers=3, kv_pools=(ctypes.c_void_p * 3)(parts[0], 66 * A, parts[1])),
+                          dict(kv_pools=None, base=64 * A, layer_stride=off)):
+                assert call(Bd, op, make(Bd, op, workspace_bytes=0, **pools)) == Bd.ERR_INVALID_ARG
+    for pools in (dict(kv_pools=(ctypes.c_void_p * 2)(64 * A, 64 * A + POOL)),
+                  dict(kv_pools=None, base=64 * A, layer_stride=POOL),
+                  dict(n_layers=1, kv_pools=None, base=64 * A, layer_stride=16)):
+        assert call(Bd, op, make(Bd, op, workspace_bytes=0, **pools)) == Bd.ERR_CAPACITY
