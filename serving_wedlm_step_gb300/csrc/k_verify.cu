@@ -458,19 +458,21 @@ verify_pick_kernel(const __grid_constant__ VerifyArgs A) {
   if (tid == 0) s_fall = kMaxDrafts + 1;
   if (kAlone) pdl_wait();
   // The inputs are read ahead of the wait: the kernel in front writes none of them, and
-  // all of its blocks were past their own wait when they let this one start.
+  // what came before it was complete when its blocks, all of them past their own wait, let
+  // this one start.  This kernel's wait does not stand between, so that the loads are taken from
+  // L2, where a finished kernel's writes are, and not from a line that L1 may still hold.
   const size_t mine = (size_t)b * A.K + tid;
-  const int x = tid < A.K ? A.tokens[mine] : -1;  // a thread a draft
-  const int n = drafts_of(A, b);
-  const float temp = A.temperature ? A.temperature[b] : 1.f;
+  const int x = tid < A.K ? __ldcg(A.tokens + mine) : -1;  // a thread a draft
+  const int n = A.n_drafts ? max(0, min(__ldcg(A.n_drafts + b), A.K)) : A.K;
+  const float temp = A.temperature ? __ldcg(A.temperature + b) : 1.f;
   bool greedy;
   const float c = log2_scale(temp, greedy);
   const bool drafted = tid < n;
   const bool token = drafted && x >= 0 && x < A.V;
-  const float zx = token ? to_f(row_of<T>(A, b, tid)[x]) : 0.f;
-  const float qx = token && A.draft_probs ? unit(__ldg(A.draft_probs + mine * A.V + x)) : 1.f;
-  const float ux = drafted ? unit(A.accept_u[mine]) : 0.f;
-  const float su = unit(A.sample_u[b]);
+  const float zx = token ? to_f(__ldcg(row_of<T>(A, b, tid) + x)) : 0.f;
+  const float qx = token && A.draft_probs ? unit(__ldcg(A.draft_probs + mine * A.V + x)) : 1.f;
+  const float ux = drafted ? unit(__ldcg(A.accept_u + mine)) : 0.f;
+  const float su = unit(__ldcg(A.sample_u + b));
   if (tid < A.K) s_x[tid] = x;
   Weigher weigh(c, temp, &s_pow);
   const SpanStat* stats = A.stats + (size_t)b * (A.K + 1) * A.spans;
