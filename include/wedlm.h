@@ -690,7 +690,11 @@ size_t wedlm_verify_drafts_workspace(const wedlm_verify_args *args);
  *    of 0..v sum to more than sample_u times the weights' sum.
  * The draw's weights are whole multiples of 2^-42 of the largest, good to 2^-29
  * (2^-32 on average) and summed in 64 bits, so that a draw does not depend on an
- * order of summation; p elsewhere is held in 32 bits.
+ * order of summation.  p elsewhere (draft_p, sampled_p and what drafts are accepted by) is
+ * held and summed in 32 bits: relative errors of some 2^-22, and of 2^-23 for each
+ * power of two that a token lies below the largest.  How a row is cut for its sum
+ * follows from B, K and V, so that in a call of another size the last bits of a
+ * p, and with them the acceptance of a draft at the very border, can be others.
  *  - mask_id has probability 0, whatever its logit.  Logits may be -inf.
  *  - A row with a NaN, a +inf or no finite logit, one whose largest logit times
  *    log2(e) / T is beyond 32-bit floating point (a row of nothing but the type's

@@ -32,15 +32,16 @@ constexpr int kGroup = 8;                     // logits of a thread's load in th
 constexpr int kStatWarps = 4;                 // of a block, a span each
 constexpr int kStatVecs = 4;                  // 16-byte loads of a thread in flight
 constexpr int kMaxRounds = 5;                 // of such loads, in a span
-constexpr int kManyWarps = 152 * 32;          // a GB300 half full of them
+constexpr int kManyWarps = 152 * 32;          // a GB300 half full of them; fixed, so that the
+                                              // workspace is the same for every device
 // Spans of a sequence, one a warp, up to which one kernel does it all: 5 x 3 drafts over 1024
 // tokens 6.1 us captured and 10.4 a call, not 6.8 and 12.1; with 32 spans and more the second
 // round of them costs what the launch does
 constexpr int kFewSpans = 16;
-// Two blocks of the draw an SM.  Swept on GB300 (calls of 15 drafts over 151936 tokens, of
-// 32 x 7 with probabilities and of 64 x 15, before the last steps): 12.4, 40.8 and 68.7 us with
-// these, 384 threads 14.9, 40.8 and 70.4, 640 12.5, 43.0 and 69.6, four blocks of 256 15.4, 51.8
-// and 71.4.  1024 threads have to wait for an empty SM.
+// Two blocks of the draw an SM.  Swept on GB300 (15 drafts over 151936 tokens, 32 x 7 with
+// probabilities, 64 x 15, captured): 10.7, 39.5 and 66.8 us with these, 384 threads 12.1, 39.7
+// and 68.4, 640 10.6, 41.5 and 68.1, four blocks of 256 11.8, 48.1 and 78.9, one of 512 10.9,
+// 45.1 and 73.7, one of 1024 12.7, 50.0 and 73.4.
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kMaxCluster = 8, kWideCluster = 16;  // the latter where the GPU has room for it
@@ -289,9 +290,10 @@ __device__ __forceinline__ SpanStat span_stat(const VerifyArgs& A, const T* row,
 }
 
 // A warp a span.  Bound by DRAM: 64 x 16 rows of 151936 bf16 logits
-// (311 MB) take 50 us, 6.2 TB/s.  Spans of 4, 5 and 6 rounds: a call of them 68.5, 67.4 and
-// 68.3 us, one of 32 x 8 rows with probabilities 41.7, 41.2 and 41.9.  Blocks an SM (and so
-// registers): 6, 7, 8, 9 and 10 70.5, 68.6, 67.8, 67.4 and 68.6 us.
+// (311 MB) take 50 us, 6.2 TB/s.  Spans of 4, 5 and 6 rounds: a call of them 67.4, 66.8 and
+// 67.1 us, one of 32 x 8 rows with probabilities 39.6, 39.5 and 40.2.  Blocks an SM (and so
+// registers): 6, 7, 8, 9 and 10 69.6, 68.0, 66.9, 66.8 and 68.3 us, the other 40.1, 39.0, 39.1,
+// 39.5 and 40.8.
 template <typename T>
 __global__ void __launch_bounds__(32 * kStatWarps, 9)
 verify_stats_kernel(const __grid_constant__ VerifyArgs A) {
@@ -433,10 +435,11 @@ template <int M> struct Mode {
 };
 
 // Bound by latency and by the weights' instructions (25 a token: 8 on pairs of floats, 10
-// on integers and moves between pairs, most of both on one pipe): of the 16 to 23 us that
-// the draw of 64 or 32 sequences takes, 3 go by until the drafts are decided, 9 to 13 on
-// the weights, the rest on the cluster's barriers, the place of the number in the sums
-// and the blocks that share an SM.
+// on integers and moves between pairs, most of both on one pipe).  From the end of the rows on,
+// 64 sequences take 16 us: 2 until the drafts are decided, 8 (median of the blocks) on the
+// weights, 1 on the number's place in the sums, the rest by blocks that share an SM.  32 with
+// probabilities 21: the last cluster of eight finds its SMs only 5 us late, then 1, 5.4
+// and 5.9 on the two passes of weights, 1 on the place.
 //
 // kAlone: the rows' spans too, where a sequence has few of them (kFewSpans); the kernel in
 // front is then the caller's.
@@ -855,8 +858,8 @@ extern "C" int wedlm_verify_drafts(const wedlm_verify_args* a, void* stream) {
   verify_split(*a, &A.rounds, &A.spans);
   const int groups = (a->vocab + 2 * (kGroup - 1)) / kGroup;
   // Blocks of a sequence: two of them fit an SM, and more of them than fit the GPU at
-  // once would only wait.  64 x 15 drafts over 151936 tokens 74 us with these four, 80 with
-  // eight, 84 with two; 32 x 7 42 with these eight, 57 with four.
+  // once would only wait.  64 x 15 drafts over 151936 tokens 66.8 us with these four, 71.7 with
+  // eight, 76.6 with two; 32 x 7 with probabilities 39.5 with these eight, 51.3 with four.
   A.cluster = 1;
   while (A.cluster < kMaxCluster &&
          (groups > kMaxGroups * A.cluster ||
